@@ -396,7 +396,7 @@ def _rstd(x, c):
         return torch.ones_like(x[..., :1])
     n = (x * x).sum(-1, keepdim=True)
     n = (n / x.shape[-1] if c["norm"] == "rms" else n) + 1e-6
-    return torch.where(n > 0, 1.0 / torch.sqrt(n), 0.0)
+    return torch.where(n == 0, 0.0, 1.0 / torch.sqrt(n))
 
 
 def _norm_fwd(s):
