@@ -18,19 +18,11 @@ namespace falcon {
 __device__ int g_dev_error = 0;
 
 namespace {
-
-// One-shot stall armed by falcon_debug_stall_next_call for the next chunk call of this thread.
-struct DebugStall {
-    bool armed = false;
-    int block = -1;
-    long long budget = kDefaultWaitBudget;
-};
-thread_local DebugStall g_stall;
-
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int *g_err_ptr[kMaxDevices] = {};
 int g_num_sms[kMaxDevices] = {};
+}  // namespace
 
 // Resolves, once per device, the device address of the error word and the SM
 // count. Returns false when the current device cannot be queried.
@@ -50,6 +42,16 @@ bool device_info(int **err, int *sms) {
     *sms = g_num_sms[dev];
     return true;
 }
+
+namespace {
+
+// One-shot stall armed by falcon_debug_stall_next_call for the next chunk call of this thread.
+struct DebugStall {
+    bool armed = false;
+    int block = -1;
+    long long budget = kDefaultWaitBudget;
+};
+thread_local DebugStall g_stall;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

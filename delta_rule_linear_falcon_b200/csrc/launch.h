@@ -7,6 +7,9 @@
 
 namespace falcon {
 
+// Resolves, once per device, the device address of the error word and the SM count (api.cu).
+bool device_info(int **err, int *sms);
+
 struct RecParams {
     int B, H, T, dk, dv, window;  // window = 1 for Falcon-1/1A
     bool regression, io_bf16;

@@ -1,0 +1,146 @@
+// ops.cuh -- device helpers of the operators around the memory.
+#pragma once
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace falcon {
+
+// V consecutive elements as one access: `raw` is what a load leaves in registers, so that a
+// prefetched value costs no conversion before it is used.
+template <typename IO, int V> struct Pack;
+
+template <> struct Pack<float, 1> {
+    typedef float raw;
+    static __device__ __forceinline__ raw ld(const float *p) { return *p; }
+    static __device__ __forceinline__ raw zero() { return 0.f; }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[1]) { x[0] = r; }
+    static __device__ __forceinline__ void st(float *p, const float (&x)[1]) { *p = x[0]; }
+};
+template <> struct Pack<float, 4> {
+    typedef float4 raw;
+    static __device__ __forceinline__ raw ld(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+    static __device__ __forceinline__ raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[4]) { x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w; }
+    static __device__ __forceinline__ void st(float *p, const float (&x)[4]) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
+template <> struct Pack<float, 8> {
+    struct raw { float4 a, b; };
+    static __device__ __forceinline__ raw ld(const float *p) {
+        return raw{reinterpret_cast<const float4 *>(p)[0], reinterpret_cast<const float4 *>(p)[1]};
+    }
+    static __device__ __forceinline__ raw zero() {
+        return raw{make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[8]) {
+        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+        x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+    }
+    static __device__ __forceinline__ void st(float *p, const float (&x)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <> struct Pack<__nv_bfloat16, 1> {
+    typedef __nv_bfloat16 raw;
+    static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *p; }
+    static __device__ __forceinline__ raw zero() { return __float2bfloat16(0.f); }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[1]) { x[0] = __bfloat162float(r); }
+    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
+};
+__device__ __forceinline__ void unpack_bf16x2(uint32_t u, float &lo, float &hi) {
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float(u & 0xffff0000u);
+}
+template <> struct Pack<__nv_bfloat16, 4> {
+    typedef uint2 raw;
+    static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
+    static __device__ __forceinline__ raw zero() { return make_uint2(0u, 0u); }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[4]) {
+        unpack_bf16x2(r.x, x[0], x[1]);
+        unpack_bf16x2(r.y, x[2], x[3]);
+    }
+    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[4]) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    }
+};
+template <> struct Pack<__nv_bfloat16, 8> {
+    typedef uint4 raw;
+    static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
+    static __device__ __forceinline__ raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[8]) {
+        unpack_bf16x2(r.x, x[0], x[1]);
+        unpack_bf16x2(r.y, x[2], x[3]);
+        unpack_bf16x2(r.z, x[4], x[5]);
+        unpack_bf16x2(r.w, x[6], x[7]);
+    }
+    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[8]) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                   pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+};
+
+template <typename E>
+__device__ __forceinline__ E *row_of(const falcon_view_t &v, long long b, long long h, long long t) {
+    return reinterpret_cast<E *>(v.p) + b * v.sb + h * v.sh + t * v.st;
+}
+
+// Tokens of sequence b: lengths[b] clamped to [0, T].
+__device__ __forceinline__ int seq_length(const int *lengths, int b, int T) {
+    return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+__device__ __forceinline__ float fast_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+__device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
+__device__ __forceinline__ float silu_grad(float x) {
+    const float g = sigmoid(x);
+    return g * (1.f + x * (1.f - g));
+}
+// log(1 + e^x); above 20 the correction e^-x is below half a step of x
+__device__ __forceinline__ float softplus(float x) { return x > 20.f ? x : log1pf(__expf(x)); }
+
+// Host: whether a view takes accesses of `bytes` bytes (pointer and strides), V elements of es bytes.
+inline bool view_packs(const falcon_view_t &v, int V, int es) {
+    if (!v.p) return true;
+    return reinterpret_cast<uintptr_t>(v.p) % (size_t)(V * es) == 0 && v.sb % V == 0 && v.sh % V == 0 && v.st % V == 0;
+}
+
+// Sums v[0..N) over NL lanes whose numbers differ by multiples of STRIDE (a power of two): as long as
+// a lane holds more than one value each step hands half of them to the partner and keeps the rest
+// (N + N/2 + ... shuffles instead of N log NL). Leaves max(1, N / NL) totals in v[0..]; returns the
+// index of the first. Where NL > N, lanes with equal index hold the same totals; `first` says which writes.
+template <int N, int NL, int STRIDE>
+__device__ __forceinline__ int lanes_sum(float (&v)[N], int lane, bool &first) {
+    int idx = 0;
+    first = true;
+    int n = N;
+#pragma unroll
+    for (int m = NL / 2; m >= 1; m >>= 1) {
+        const bool hi = (lane & (m * STRIDE)) != 0;
+        if (n > 1) {
+            n >>= 1;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i < n) {
+                    const float send = hi ? v[i] : v[i + n];
+                    const float keep = hi ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m * STRIDE);
+                }
+            }
+            if (hi) idx += n;
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m * STRIDE);
+            if (hi) first = false;
+        }
+    }
+    return idx;
+}
+
+}  // namespace falcon

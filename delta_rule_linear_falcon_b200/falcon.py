@@ -7,6 +7,7 @@ there is no fallback, so a missing library raises at the first call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,6 +23,13 @@ FALCON_RULE_1, FALCON_RULE_1A, FALCON_RULE_3, FALCON_RULE_3A = 1, 2, 3, 4
 FALCON_RULE_2, FALCON_RULE_2A = 5, 6
 FALCON_F32, FALCON_BF16 = 0, 1
 FALCON_SAME_STEP = 0x100  # OR into a rule code: pair (k_t, v_t) at step t (same-step association)
+FALCON_ACT_NONE, FALCON_ACT_SILU = 0, 1
+FALCON_SCAN_SOFTPLUS = 1
+FALCON_NORM_NONE, FALCON_NORM_RMS, FALCON_NORM_L2 = 0, 1, 2
+FALCON_ROT_HALF, FALCON_ROT_PAIRS = 0, 1
+ACTS = {"none": FALCON_ACT_NONE, "silu": FALCON_ACT_SILU}
+NORMS = {"none": FALCON_NORM_NONE, "rms": FALCON_NORM_RMS, "l2": FALCON_NORM_L2}
+ROTS = {"half": FALCON_ROT_HALF, "pairs": FALCON_ROT_PAIRS}
 RULES = {"falcon1": FALCON_RULE_1, "falcon1a": FALCON_RULE_1A, "falcon3": FALCON_RULE_3,
          "falcon3a": FALCON_RULE_3A, "falcon2": FALCON_RULE_2, "falcon2a": FALCON_RULE_2A}
 
@@ -57,6 +65,56 @@ class FalconGrads(ctypes.Structure):
     ]
 
 
+_I, _P, _F32, _LL = ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_longlong
+
+
+class FalconView(ctypes.Structure):
+    """Mirror of falcon_view_t."""
+    _fields_ = [("p", _P), ("sb", _LL), ("sh", _LL), ("st", _LL)]
+
+
+class FalconConvArgs(ctypes.Structure):
+    """Mirror of falcon_conv_args_t."""
+    _fields_ = [("io_dtype", _I), ("B", _I), ("H", _I), ("T", _I), ("d", _I), ("K", _I), ("act", _I),
+                ("x", FalconView), ("y", FalconView), ("w", _P), ("bias", _P), ("lengths", _P),
+                ("state", _P), ("state_out", _P)]
+
+
+class FalconConvGrads(ctypes.Structure):
+    """Mirror of falcon_conv_grads_t."""
+    _fields_ = [("dy", FalconView), ("dstate_out", _P), ("dx", FalconView), ("dw", _P), ("dbias", _P),
+                ("dstate", _P)]
+
+
+class FalconScanArgs(ctypes.Structure):
+    """Mirror of falcon_scan_args_t."""
+    _fields_ = [("io_dtype", _I), ("B", _I), ("H", _I), ("T", _I), ("dk", _I), ("dv", _I), ("flags", _I),
+                ("q", FalconView), ("k", FalconView), ("v", FalconView), ("delta", FalconView),
+                ("z", FalconView), ("o", FalconView), ("A", _P), ("D", _P), ("delta_bias", _P),
+                ("lengths", _P), ("S0", _P), ("S_out", _P)]
+
+
+class FalconScanGrads(ctypes.Structure):
+    """Mirror of falcon_scan_grads_t."""
+    _fields_ = [("dO", FalconView), ("dS_T", _P), ("dq", FalconView), ("dk", FalconView), ("dv", FalconView),
+                ("ddelta", FalconView), ("dz", FalconView), ("dA", _P), ("dD", _P), ("ddelta_bias", _P),
+                ("dS0", _P)]
+
+
+class FalconQknormArgs(ctypes.Structure):
+    """Mirror of falcon_qknorm_args_t."""
+    _fields_ = [("io_dtype", _I), ("B", _I), ("Hq", _I), ("Hk", _I), ("T", _I), ("d", _I), ("norm", _I),
+                ("rot", _I), ("rot_layout", _I), ("q", FalconView), ("k", FalconView), ("q_out", FalconView),
+                ("k_out", FalconView), ("wq", _P), ("wk", _P), ("eps", _F32), ("freq", _P),
+                ("positions", _P), ("lengths", _P)]
+
+
+class FalconQknormGrads(ctypes.Structure):
+    """Mirror of falcon_qknorm_grads_t."""
+    _fields_ = [("dq_out", FalconView), ("dk_out", FalconView), ("dq", FalconView), ("dk", FalconView),
+                ("dwq", _P), ("dwk", _P)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -84,6 +142,20 @@ def lib() -> ctypes.CDLL:
             L.falcon_bwd_recurrent.restype = i
             L.falcon_decode_step.argtypes = [i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, f, vp, vp]
             L.falcon_decode_step.restype = i
+            for name, args, grads in (("conv", FalconConvArgs, FalconConvGrads), ("scan", FalconScanArgs, FalconScanGrads),
+                                      ("qknorm", FalconQknormArgs, FalconQknormGrads)):
+                A, G = ctypes.POINTER(args), ctypes.POINTER(grads)
+                fwd, bwd = getattr(L, f"falcon_{name}_fwd"), getattr(L, f"falcon_{name}_bwd")
+                fwd.argtypes = [A, vp, ctypes.c_size_t, vp] if name == "scan" else [A, vp]
+                bwd.argtypes = [A, G, vp, ctypes.c_size_t, vp]
+                fwd.restype = bwd.restype = i
+                size = getattr(L, f"falcon_{name}_bwd_workspace_size")
+                size.argtypes, size.restype = [A], ctypes.c_size_t
+                if name != "qknorm":
+                    step = getattr(L, f"falcon_{name}_step")
+                    step.argtypes, step.restype = [A, vp], i
+            L.falcon_scan_workspace_size.argtypes = [ctypes.POINTER(FalconScanArgs)]
+            L.falcon_scan_workspace_size.restype = ctypes.c_size_t
             L.falcon_status_string.argtypes = [i]
             L.falcon_status_string.restype = ctypes.c_char_p
             L.falcon_check_device_errors.argtypes = [vp]
@@ -280,6 +352,324 @@ def falcon_decode_step(S, k_prev, q, k, v, alpha, eta, *, rule="falcon1", eps=1e
     if st != FALCON_OK:
         raise FalconError(st, "falcon_decode_step")
     return o
+
+
+# ---- operators around the memory: convolution, selective scan, q/k norm ------------------------------
+#
+# Sequence tensors are (B, H, T, d) torch views of any batch, head and token strides whose last axis is
+# contiguous (a transposed slice of a fused projection goes in as it is). Every tensor of a call is on one
+# device, which need not be the current one. Outputs and workspaces that a call makes are allocated on
+# `stream` (default: the device's current stream), where its kernels run.
+
+def _on(dev, stream):
+    """The context in which a call allocates, and the raw stream on which it launches."""
+    if stream is None:
+        ctx = contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return ctx, torch.cuda.current_stream(dev).cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _tensor(t, name, shape, dtype, dev):
+    """Refuses what is not a tensor of this shape, type and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _seq(t, name, shape, dtype, dev):
+    """falcon_view_t of a (B, H, T, d) tensor, or of a (B, H, d) one as a single token."""
+    if t is None:
+        return FalconView()
+    _tensor(t, name, shape, dtype, dev)
+    s = t.stride()
+    if shape[-1] > 1 and s[-1] != 1 and t.numel() > 0:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return FalconView(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
+
+
+def _arr(t, name, shape, dtype, dev):
+    """Address of a contiguous parameter, state or gradient, or None."""
+    if t is None:
+        return None
+    _tensor(t, name, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _code(table, key, what) -> int:
+    if key not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, got {key!r}")
+    return table[key]
+
+
+def _rank(t, name, rank):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != rank:
+        raise ValueError(f"{name} must have {rank} axes, got the shape {tuple(t.shape)}")
+
+
+def _call(name, *args):
+    st = getattr(lib(), name)(*args)
+    if st != FALCON_OK:
+        raise FalconError(st, name)
+
+
+def _workspace(workspace, need, dev):
+    """(tensor, address, bytes) of the caller's workspace or of one made here."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace")
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, other tensors on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _conv_args(x, w, bias, act, state, lengths, shape):
+    dev, io, f32 = x.device, x.dtype, torch.float32
+    B, H, d = shape[0], shape[1], shape[-1]
+    T = shape[2] if len(shape) == 4 else 1
+    _rank(w, "w", 3)
+    K = w.shape[2]
+    a = FalconConvArgs(_dtype_code(x), B, H, T, d, K, _code(ACTS, act, "act"))
+    a.x = _seq(x, "x", shape, io, dev)
+    a.w = _arr(w, "w", (H, d, K), f32, dev)
+    a.bias = _arr(bias, "bias", (H, d), f32, dev)
+    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
+    a.state = _arr(state, "state", (B, H, max(K - 1, 0), d), io, dev)
+    return a, K
+
+
+def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=None, state_out=None,
+                    want_state=False, stream=None):
+    """Causal depthwise convolution over the last K tokens: x (B, H, T, d), w (H, d, K) fp32. Returns
+    (y, state_out); y is head-major (B, H, T, d) unless given, state_out (B, H, K - 1, d) is the last
+    K - 1 inputs, made where want_state asks for it (it may be `state` itself). With ``lengths`` (B,)
+    int32, rows of y behind a sequence's end are left as they were (uninitialised in a y made here)."""
+    _rank(x, "x", 4)
+    a, K = _conv_args(x, w, bias, act, state, lengths, tuple(x.shape))
+    B, H, T, d = x.shape
+    ctx, raw = _on(x.device, stream)
+    with ctx:
+        if y is None:
+            y = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+        if state_out is None and want_state:
+            state_out = torch.empty((B, H, K - 1, d), dtype=x.dtype, device=x.device)
+        a.y = _seq(y, "y", (B, H, T, d), x.dtype, x.device)
+        a.state_out = _arr(state_out, "state_out", (B, H, K - 1, d), x.dtype, x.device)
+        _call("falcon_conv_fwd", ctypes.byref(a), raw)
+    return y, state_out
+
+
+def falcon_conv_step(x, w, state, *, bias=None, act="silu", state_out=None, y=None, stream=None):
+    """One token of the convolution for N sequences: x (N, H, d), state (N, H, K - 1, d), which is updated
+    in place unless state_out is given. Returns y (N, H, d)."""
+    _rank(x, "x", 3)
+    shape = tuple(x.shape)
+    a, K = _conv_args(x, w, bias, act, state, None, shape)
+    state_out = state if state_out is None else state_out
+    a.state_out = _arr(state_out, "state_out", (shape[0], shape[1], K - 1, shape[2]), x.dtype, x.device)
+    ctx, raw = _on(x.device, stream)
+    with ctx:
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        a.y = _seq(y, "y", shape, x.dtype, x.device)
+        _call("falcon_conv_step", ctypes.byref(a), raw)
+    return y
+
+
+def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None, dstate_out=None, dx=None,
+                    workspace=None, stream=None):
+    """Gradients of falcon_conv_fwd for dy (B, H, T, d) fp32 and dstate_out (B, H, K - 1, d) fp32 or None.
+    Returns a dict of fp32 tensors dx (in x's axis order, token-major like a projection's rows, unless given),
+    dw, dbias (None without bias) and dstate (None without state)."""
+    _rank(x, "x", 4)
+    f32, dev = torch.float32, x.device
+    a, K = _conv_args(x, w, bias, act, state, lengths, tuple(x.shape))
+    B, H, T, d = x.shape
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if dx is None:
+            dx = torch.empty((B, T, H, d), dtype=f32, device=dev).transpose(1, 2)
+        out = {"dx": dx, "dw": torch.empty((H, d, K), dtype=f32, device=dev),
+               "dbias": torch.empty((H, d), dtype=f32, device=dev) if bias is not None else None,
+               "dstate": torch.empty((B, H, K - 1, d), dtype=f32, device=dev) if state is not None else None}
+        g = FalconConvGrads()
+        g.dy = _seq(dy, "dy", (B, H, T, d), f32, dev)
+        g.dx = _seq(dx, "dx", (B, H, T, d), f32, dev)
+        g.dstate_out = _arr(dstate_out, "dstate_out", (B, H, K - 1, d), f32, dev)
+        g.dw, g.dbias, g.dstate = _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"])
+        need = int(lib().falcon_conv_bwd_workspace_size(ctypes.byref(a)))
+        workspace, p, n = _workspace(workspace, need, dev)
+        _call("falcon_conv_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+    return out
+
+
+def _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, step):
+    rank = 3 if step else 4
+    _rank(v, "v", rank)
+    _rank(k, "k", rank)
+    vs, ks = tuple(v.shape), tuple(k.shape)
+    dev, io, f32 = v.device, v.dtype, torch.float32
+    B, H, dv, dk = vs[0], vs[1], vs[-1], ks[-1]
+    T = 1 if step else vs[2]
+    ks = vs[:-1] + (dk,)
+    a = FalconScanArgs(_dtype_code(v), B, H, T, dk, dv, FALCON_SCAN_SOFTPLUS if softplus else 0)
+    a.q, a.k = _seq(q, "q", ks, io, dev), _seq(k, "k", ks, io, dev)
+    a.v, a.delta = _seq(v, "v", vs, io, dev), _seq(delta, "delta", vs, io, dev)
+    a.z = _seq(z, "z", vs, io, dev)
+    a.A = _arr(A, "A", (H, dv, dk), f32, dev)
+    a.D = _arr(D, "D", (H, dv), f32, dev)
+    a.delta_bias = _arr(delta_bias, "delta_bias", (H, dv), f32, dev)
+    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
+    a.S0 = _arr(S0, "S0", (B, H, dv, dk), f32, dev)
+    return a, (B, H, T, dk, dv)
+
+
+def falcon_scan_workspace_size(args: FalconScanArgs) -> int:
+    return int(lib().falcon_scan_workspace_size(ctypes.byref(args)))
+
+
+def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softplus=True, S0=None, lengths=None,
+                    o=None, S_out=None, want_state=True, workspace=None, stream=None):
+    """Selective scan: q, k (B, H, T, dk), v, delta and z (B, H, T, dv), A (H, dv, dk), D and delta_bias
+    (H, dv), S0 (B, H, dv, dk); parameters and states fp32. Returns (o, S_out). With few channels the
+    sequence is split, for which a workspace is made here unless one is given (a smaller one runs it whole)."""
+    a, (B, H, T, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, False)
+    dev = v.device
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if o is None:
+            o = torch.empty((B, H, T, dv), dtype=v.dtype, device=dev)
+        if S_out is None and want_state:
+            S_out = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        a.o = _seq(o, "o", (B, H, T, dv), v.dtype, dev)
+        a.S_out = _arr(S_out, "S_out", (B, H, dv, dk), torch.float32, dev)
+        workspace, p, n = _workspace(workspace, falcon_scan_workspace_size(a) if workspace is None else 0, dev)
+        _call("falcon_scan_fwd", ctypes.byref(a), p, n, raw)
+    return o, S_out
+
+
+def falcon_scan_step(q, k, v, delta, A, S, *, D=None, z=None, delta_bias=None, softplus=True, S_out=None, o=None,
+                     stream=None):
+    """One token of the scan for N sequences: q, k (N, H, dk), v, delta, z (N, H, dv); S (N, H, dv, dk) fp32 is
+    updated in place unless S_out is given. Returns o (N, H, dv)."""
+    a, (B, H, _, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, None, S, True)
+    dev = v.device
+    a.S_out = _arr(S if S_out is None else S_out, "S_out", (B, H, dv, dk), torch.float32, dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        if o is None:
+            o = torch.empty((B, H, dv), dtype=v.dtype, device=dev)
+        a.o = _seq(o, "o", (B, H, dv), v.dtype, dev)
+        _call("falcon_scan_step", ctypes.byref(a), raw)
+    return o
+
+
+def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, softplus=True, S0=None, lengths=None,
+                    dS_T=None, workspace=None, stream=None):
+    """Gradients of falcon_scan_fwd for dO (B, H, T, dv) fp32 and dS_T (B, H, dv, dk) fp32 or None. Returns a
+    dict of fp32 tensors dq, dk, dv, ddelta, dA and, for the inputs that were given, dD, ddelta_bias, dz, dS0
+    (None otherwise). Sequence gradients are token-major rows seen as (B, H, T, d)."""
+    a, (B, H, T, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, False)
+    dev, f32 = v.device, torch.float32
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        rows = lambda d: torch.empty((B, T, H, d), dtype=f32, device=dev).transpose(1, 2)
+        out = {"dq": rows(dk), "dk": rows(dk), "dv": rows(dv), "ddelta": rows(dv),
+               "dz": rows(dv) if z is not None else None,
+               "dA": torch.empty((H, dv, dk), dtype=f32, device=dev),
+               "dD": torch.empty((H, dv), dtype=f32, device=dev) if D is not None else None,
+               "ddelta_bias": torch.empty((H, dv), dtype=f32, device=dev) if delta_bias is not None else None,
+               "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if S0 is not None else None}
+        g = FalconScanGrads()
+        g.dO = _seq(dO, "dO", (B, H, T, dv), f32, dev)
+        g.dS_T = _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev)
+        for n, d in (("dq", dk), ("dk", dk), ("dv", dv), ("ddelta", dv), ("dz", dv)):
+            setattr(g, n, _seq(out[n], n, (B, H, T, d), f32, dev))
+        for n in ("dA", "dD", "ddelta_bias", "dS0"):
+            setattr(g, n, _ptr(out[n]))
+        need = int(lib().falcon_scan_bwd_workspace_size(ctypes.byref(a)))
+        workspace, p, n = _workspace(workspace, need, dev)
+        _call("falcon_scan_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+    return out
+
+
+def _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths):
+    """q or k may be None (no heads of it)."""
+    x = q if q is not None else k
+    if x is None:
+        raise TypeError("q or k must be given")
+    for t, n in ((q, "q"), (k, "k")):
+        if t is not None:
+            _rank(t, n, 4)
+    dev, io, f32 = x.device, x.dtype, torch.float32
+    B, _, T, d = x.shape
+    qs = (B, q.shape[1] if q is not None else 0, T, d)
+    ks = (B, k.shape[1] if k is not None else 0, T, d)
+    rot = int(rot)
+    a = FalconQknormArgs(_dtype_code(x), B, qs[1], ks[1], T, d, _code(NORMS, norm, "norm"), rot,
+                         _code(ROTS, layout, "layout"))
+    a.q, a.k = _seq(q, "q", qs, io, dev), _seq(k, "k", ks, io, dev)
+    a.wq, a.wk = _arr(wq, "wq", (d,), f32, dev), _arr(wk, "wk", (d,), f32, dev)
+    a.eps = float(eps)
+    a.freq = _arr(freq, "freq", (rot // 2,), f32, dev)
+    a.positions = _arr(positions, "positions", (B, T), torch.int32, dev)
+    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
+    return a, qs, ks
+
+
+def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, layout="half", freq=None, positions=None,
+                      lengths=None, q_out=None, k_out=None, stream=None):
+    """Norm of each head's rows of q (B, Hq, T, d) and k (B, Hk, T, d) with the rotation of their first ``rot``
+    channels by positions (B, T) int32 (default: 0, 1, ..) times freq (rot / 2) fp32. Either of q and k may be
+    None. Returns (q_out, k_out), head-major unless given; q_out may be q itself, k_out k."""
+    a, qs, ks = _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
+    x = q if q is not None else k
+    ctx, raw = _on(x.device, stream)
+    with ctx:
+        if q_out is None and q is not None:
+            q_out = torch.empty(qs, dtype=x.dtype, device=x.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(ks, dtype=x.dtype, device=x.device)
+        a.q_out, a.k_out = _seq(q_out, "q_out", qs, x.dtype, x.device), _seq(k_out, "k_out", ks, x.dtype, x.device)
+        _call("falcon_qknorm_fwd", ctypes.byref(a), raw)
+    return q_out, k_out
+
+
+def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, layout="half", freq=None,
+                      positions=None, lengths=None, workspace=None, stream=None):
+    """Gradients of falcon_qknorm_fwd for dq_out, dk_out (fp32, the shapes of q and k). Returns a dict of fp32
+    tensors dq, dk (token-major rows seen as (B, H, T, d); None where q or k is), dwq and dwk (None without
+    the weight)."""
+    a, qs, ks = _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
+    dev, f32 = (q if q is not None else k).device, torch.float32
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        rows = lambda s: torch.empty((s[0], s[2], s[1], s[3]), dtype=f32, device=dev).transpose(1, 2)
+        out = {"dq": rows(qs) if q is not None else None, "dk": rows(ks) if k is not None else None,
+               "dwq": torch.empty(qs[3:], dtype=f32, device=dev) if wq is not None else None,
+               "dwk": torch.empty(qs[3:], dtype=f32, device=dev) if wk is not None else None}
+        g = FalconQknormGrads()
+        g.dq_out, g.dk_out = _seq(dq_out, "dq_out", qs, f32, dev), _seq(dk_out, "dk_out", ks, f32, dev)
+        g.dq, g.dk = _seq(out["dq"], "dq", qs, f32, dev), _seq(out["dk"], "dk", ks, f32, dev)
+        g.dwq, g.dwk = _ptr(out["dwq"]), _ptr(out["dwk"])
+        need = int(lib().falcon_qknorm_bwd_workspace_size(ctypes.byref(a))) if wq is not None or wk is not None else 0
+        workspace, p, n = _workspace(workspace, need, dev)
+        _call("falcon_qknorm_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+    return out
 
 
 def falcon_debug_stall_next_call(block: int, wait_budget_cycles: int) -> int:

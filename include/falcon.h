@@ -304,6 +304,216 @@ FALCON_API falcon_status_t falcon_decode_step(int rule, int io_dtype, int N, int
                                    const void *v, const float *alpha, const float *eta,
                                    float eps, void *o, falcon_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the memory: the short causal convolution that its q, k and v pass through,
+ * the norm of queries and keys with the position rotation, and the selective scan, a recurrence
+ * with a decay of its own for every entry of the state.
+ *
+ * Conventions of these entry points, besides the ones above:
+ *  - Sequence tensors are views: element (b, h, t, i) of a tensor is p[b*sb + h*sh + t*st + i],
+ *    strides in elements, the innermost axis contiguous. A slice of a fused projection
+ *    (token-major rows) goes in as it lies, and an output can be written head-major for
+ *    falcon_fwd_chunk. Strides are >= 0 (0 repeats an input along that axis; the elements of
+ *    an output or gradient must not overlap). Pointers of views need the alignment of their
+ *    element only; when pointers and strides are 16-byte multiples, wider accesses are used.
+ *  - Outputs and gradients must not overlap inputs or each other, except where an entry point
+ *    says so.
+ *  - Parameters (weights, biases, A, D, frequencies) and all gradients are fp32, whatever
+ *    io_dtype is; gradients are views too where the tensor they belong to is one.
+ *  - `lengths`: NULL, or B int32 on the device. Sequence b then has lengths[b] tokens (clamped to
+ *    [0, T]); what lies at t >= lengths[b] is not read, rows of forward outputs there are left as
+ *    they were, rows of gradients there are written 0, and final states are those after the last
+ *    token of the sequence.
+ *  - Sums over tokens are taken in a fixed order: repeated calls give the same bits.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+    void *p;              /* device memory, or NULL where the tensor is optional */
+    long long sb, sh, st; /* strides of batch, head and token, in elements        */
+} falcon_view_t;
+
+typedef enum { FALCON_ACT_NONE = 0, FALCON_ACT_SILU = 1 } falcon_act_t;
+
+/*
+ * falcon_conv_fwd -- causal depthwise convolution over the last K tokens:
+ *   p_t = bias + sum_{j<K} w_j x_{t-K+1+j},   y_t = act(p_t)
+ * for every channel of every head. x_{-1} .. x_{-(K-1)} come from `state` (the last K-1 inputs
+ * before this segment, oldest first) or are 0. `state_out` gets the last K-1 inputs of the
+ * extended sequence; it may be the same memory as `state`.
+ * Supported: 1 <= K <= 8; any d >= 1; fp32 or bf16. Sums in fp32, one rounding at the end.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+typedef struct {
+    int io_dtype;         /* falcon_dtype_t of x, y, state and state_out            */
+    int B, H, T, d;       /* batch, heads, tokens (T >= 0), channels of a head       */
+    int K;                /* taps                                                    */
+    int act;              /* falcon_act_t                                            */
+    falcon_view_t x;      /* (B,H,T,d)                                               */
+    falcon_view_t y;      /* (B,H,T,d) output                                        */
+    const float *w;       /* (H,d,K); w[..., K-1] multiplies the current token       */
+    const float *bias;    /* (H,d) or NULL                                           */
+    const int *lengths;   /* (B) or NULL                                             */
+    const void *state;    /* (B,H,K-1,d) or NULL for zeros                           */
+    void *state_out;      /* (B,H,K-1,d) or NULL                                     */
+} falcon_conv_args_t;
+
+FALCON_API falcon_status_t falcon_conv_fwd(const falcon_conv_args_t *args, falcon_stream_t stream);
+
+/*
+ * falcon_conv_step -- one token for B sequences: falcon_conv_fwd with T = 1, as one small kernel.
+ * `state` and `state_out` are both required (the same memory updates the cache in place);
+ * `lengths` must be NULL. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+FALCON_API falcon_status_t falcon_conv_step(const falcon_conv_args_t *args, falcon_stream_t stream);
+
+/*
+ * falcon_conv_bwd -- gradients of falcon_conv_fwd. With dp_t = dy_t act'(p_t):
+ *   dx_t = sum_j w_j dp_{t+K-1-j};  dw_j = sum_{b,t} dp_t x_{t-K+1+j};  dbias = sum_{b,t} dp_t;
+ *   dstate is dx at the cached tokens; dstate_out adds to the tokens that state_out copied.
+ * args->y and args->state_out are ignored. dbias is written when not NULL (args->bias may be
+ * NULL), dstate when not NULL (args->state may be NULL).
+ * Workspace: falcon_conv_bwd_workspace_size(args) bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+typedef struct {
+    falcon_view_t dy;         /* (B,H,T,d) fp32                       */
+    const float *dstate_out;  /* (B,H,K-1,d) or NULL (zero)           */
+    falcon_view_t dx;         /* (B,H,T,d) fp32, written              */
+    float *dw;                /* (H,d,K), written                     */
+    float *dbias;             /* (H,d) or NULL                        */
+    float *dstate;            /* (B,H,K-1,d) or NULL                  */
+} falcon_conv_grads_t;
+
+FALCON_API size_t falcon_conv_bwd_workspace_size(const falcon_conv_args_t *args);
+FALCON_API falcon_status_t falcon_conv_bwd(const falcon_conv_args_t *args, const falcon_conv_grads_t *grads,
+                                           void *workspace, size_t workspace_bytes, falcon_stream_t stream);
+
+/*
+ * falcon_scan_fwd -- selective scan: per head a d_v x d_k state whose entry (i, c) decays at a
+ * rate of its own, over steps that the input chooses:
+ *   dt_t[i]   = softplus(delta_t[i] + delta_bias[i])   (FALCON_SCAN_SOFTPLUS; else delta_t[i] + delta_bias[i])
+ *   S_t[i,c]  = exp(dt_t[i] A[i,c]) S_{t-1}[i,c] + dt_t[i] v_t[i] k_t[c]
+ *   o_t[i]    = (sum_c S_t[i,c] q_t[c] + D[i] v_t[i]) silu(z_t[i])
+ * (the terms of D, delta_bias and z only where those are given). dt A <= 0 is a precondition: the
+ * decays lie in [0, 1]; it is not checked per element. The state, the decays and all sums are fp32.
+ * Supported: 1 <= dk <= 128; any dv >= 1; fp32 or bf16.
+ * Workspace: with few channels the sequence is split into segments that run at once, in three
+ * steps (each segment from a zero state, the states between them, each segment from its state).
+ * falcon_scan_workspace_size(args) bytes, 16-byte aligned, are needed for that, 0 where it does not
+ * pay; with less, or NULL, the sequence is not split. Results differ by rounding only.
+ * S_out may be the same memory as S0. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+#define FALCON_SCAN_SOFTPLUS 1
+
+typedef struct {
+    int io_dtype;            /* falcon_dtype_t of q, k, v, delta, z and o            */
+    int B, H, T;             /* batch, heads, tokens (T >= 0)                        */
+    int dk, dv;              /* columns and rows (channels) of a head's state        */
+    int flags;               /* FALCON_SCAN_SOFTPLUS or 0                            */
+    falcon_view_t q, k;      /* (B,H,T,dk)                                           */
+    falcon_view_t v, delta;  /* (B,H,T,dv)                                           */
+    falcon_view_t z;         /* (B,H,T,dv) or p = NULL                               */
+    falcon_view_t o;         /* (B,H,T,dv) output                                    */
+    const float *A;          /* (H,dv,dk)                                            */
+    const float *D;          /* (H,dv) or NULL                                       */
+    const float *delta_bias; /* (H,dv) or NULL                                       */
+    const int *lengths;      /* (B) or NULL                                          */
+    const float *S0;         /* (B,H,dv,dk) initial state, or NULL for zero          */
+    float *S_out;            /* (B,H,dv,dk) final state, or NULL                     */
+} falcon_scan_args_t;
+
+FALCON_API size_t falcon_scan_workspace_size(const falcon_scan_args_t *args);
+FALCON_API falcon_status_t falcon_scan_fwd(const falcon_scan_args_t *args, void *workspace,
+                                           size_t workspace_bytes, falcon_stream_t stream);
+
+/*
+ * falcon_scan_step -- one token for B sequences: falcon_scan_fwd with T = 1 as one kernel, bound by
+ * reading and writing the state. S0 and S_out are both required (the same memory updates the
+ * state in place); `lengths` must be NULL. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+FALCON_API falcon_status_t falcon_scan_step(const falcon_scan_args_t *args, falcon_stream_t stream);
+
+/*
+ * falcon_scan_bwd -- gradients of falcon_scan_fwd. With a_t = exp(dt_t A), dy_t = dO_t silu(z_t) and
+ * G_t = dy_t q_t^T + a_{t+1} G_{t+1} (G behind the last token: dS_T):
+ *   dq_t[c] = sum_i dy_t[i] S_t[i,c];            dk_t[c] = sum_i G_t[i,c] dt_t[i] v_t[i];
+ *   dv_t[i] = dt_t[i] sum_c G_t[i,c] k_t[c] + D[i] dy_t[i];
+ *   ddt_t[i] = sum_c G_t[i,c] (A[i,c] a_t[i,c] S_{t-1}[i,c] + v_t[i] k_t[c]), times the softplus' slope;
+ *   dA = sum_{b,t} G_t dt_t a_t S_{t-1};  dD = sum_{b,t} dy_t v_t;  dS0 = a_1 G_1;
+ *   dz_t[i] = dO_t[i] (sum_c S_t q_t + D v_t) silu'(z_t).
+ * args->o and args->S_out are ignored. Optional gradients are written when not NULL; dz only with z.
+ * q and k shared by heads (stride 0) get a gradient for each head, which the caller adds up.
+ * Workspace: falcon_scan_bwd_workspace_size(args) bytes, 16-byte aligned (states and their gradients
+ * between segments of a fixed length, and partial sums).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+typedef struct {
+    falcon_view_t dO;      /* (B,H,T,dv) fp32                      */
+    const float *dS_T;     /* (B,H,dv,dk) or NULL (zero)           */
+    falcon_view_t dq, dk;  /* (B,H,T,dk) fp32, written             */
+    falcon_view_t dv;      /* (B,H,T,dv) fp32, written             */
+    falcon_view_t ddelta;  /* (B,H,T,dv) fp32, written             */
+    falcon_view_t dz;      /* (B,H,T,dv) fp32, or p = NULL         */
+    float *dA;             /* (H,dv,dk), written                   */
+    float *dD;             /* (H,dv) or NULL                       */
+    float *ddelta_bias;    /* (H,dv) or NULL                       */
+    float *dS0;            /* (B,H,dv,dk) or NULL                  */
+} falcon_scan_grads_t;
+
+FALCON_API size_t falcon_scan_bwd_workspace_size(const falcon_scan_args_t *args);
+FALCON_API falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *args, const falcon_scan_grads_t *grads,
+                                           void *workspace, size_t workspace_bytes, falcon_stream_t stream);
+
+/*
+ * falcon_qknorm_fwd -- norm of each head's query and key rows, with the rotation by position in
+ * the same pass (what falcon_fwd_* expects of q and k is up to the layer; these are the usual ones):
+ *   FALCON_NORM_RMS: n = x w / sqrt(mean(x^2) + eps);  FALCON_NORM_L2: n = x w / sqrt(sum(x^2) + eps);
+ *   FALCON_NORM_NONE: n = x w   (w only where given; a row whose root is 0 gives 0)
+ * then the first `rot` channels of n turn in pairs by the angle positions[b,t] freq[j]:
+ *   pair j is (j, j + rot/2) for FALCON_ROT_HALF, (2j, 2j+1) for FALCON_ROT_PAIRS;
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin).
+ * Angles are reduced in fp64, so far positions keep their accuracy; everything else is fp32.
+ * positions NULL: t. rot = 0: no rotation. Hk (or Hq) = 0 leaves out that tensor. q_out may be the
+ * same memory as q with the same strides (likewise k). One token per sequence is T = 1.
+ * Supported: 1 <= d <= 256; rot even, 0 <= rot <= d; fp32 or bf16.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+typedef enum { FALCON_NORM_NONE = 0, FALCON_NORM_RMS = 1, FALCON_NORM_L2 = 2 } falcon_norm_t;
+typedef enum { FALCON_ROT_HALF = 0, FALCON_ROT_PAIRS = 1 } falcon_rot_t;
+
+typedef struct {
+    int io_dtype;               /* falcon_dtype_t of q, k, q_out and k_out                */
+    int B, Hq, Hk, T, d;        /* batch, heads of q and of k, tokens, width              */
+    int norm;                   /* falcon_norm_t                                          */
+    int rot, rot_layout;        /* rotated channels, falcon_rot_t                         */
+    falcon_view_t q, k;         /* (B,Hq,T,d), (B,Hk,T,d)                                 */
+    falcon_view_t q_out, k_out; /* outputs of the same shapes                             */
+    const float *wq, *wk;       /* (d) or NULL                                            */
+    float eps;                  /* >= 0                                                   */
+    const float *freq;          /* (rot/2) angle per position, or NULL when rot = 0       */
+    const int *positions;       /* (B,T) int32 or NULL                                    */
+    const int *lengths;         /* (B) or NULL                                            */
+} falcon_qknorm_args_t;
+
+FALCON_API falcon_status_t falcon_qknorm_fwd(const falcon_qknorm_args_t *args, falcon_stream_t stream);
+
+/*
+ * falcon_qknorm_bwd -- gradients of falcon_qknorm_fwd: with g the upstream row turned back by its
+ * angles and xr = x / root:  dw = sum g xr;  u = g w;  dx = (u - xr mean(u xr)) / root (the sum in place
+ * of the mean for FALCON_NORM_L2; dx = u for FALCON_NORM_NONE). args->q_out and k_out are ignored.
+ * dq may be the same memory as dq_out with the same strides (likewise dk).
+ * Workspace: falcon_qknorm_bwd_workspace_size(args) bytes, 16-byte aligned (0 without dwq and dwk).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+typedef struct {
+    falcon_view_t dq_out, dk_out; /* (B,Hq,T,d), (B,Hk,T,d) fp32          */
+    falcon_view_t dq, dk;         /* the same shapes, fp32, written        */
+    float *dwq, *dwk;             /* (d) or NULL                           */
+} falcon_qknorm_grads_t;
+
+FALCON_API size_t falcon_qknorm_bwd_workspace_size(const falcon_qknorm_args_t *args);
+FALCON_API falcon_status_t falcon_qknorm_bwd(const falcon_qknorm_args_t *args, const falcon_qknorm_grads_t *grads,
+                                             void *workspace, size_t workspace_bytes, falcon_stream_t stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 FALCON_API const char *falcon_status_string(falcon_status_t status);
 
