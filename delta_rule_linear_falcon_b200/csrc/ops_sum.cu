@@ -5,13 +5,13 @@ namespace falcon {
 
 namespace {
 
-constexpr int kSumCols = 32, kSumChains = 16;
+constexpr int kSumCols = 32, kSumChains = 32;
 
 struct SumJobs {
     SumJob job[4];
 };
 
-// 32 columns a block (one 128-byte line of each row), 16 chains over the rows joined in a fixed order.
+// 32 columns a block (one 128-byte line of each row), 32 chains over the rows joined in a fixed order.
 __global__ void __launch_bounds__(kSumCols * kSumChains) column_sum_kernel(SumJobs jobs, long long nparts) {
     __shared__ float acc[kSumChains][kSumCols + 1];
     const SumJob j = jobs.job[blockIdx.y];
@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(kSumCols * kSumChains) column_sum_kernel(SumJo
     if ((long long)blockIdx.x * kSumCols >= j.n) return;
     float s = 0.f;
     if (e < j.n) {
-#pragma unroll 4
+#pragma unroll 8
         for (long long p = threadIdx.y; p < nparts; p += kSumChains) s += j.part[p * j.stride + e];
     }
     acc[threadIdx.y][threadIdx.x] = s;

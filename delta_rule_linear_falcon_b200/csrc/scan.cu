@@ -28,6 +28,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
     constexpr int CPB = kScanThreads / SL;           // channels of a block
     constexpr int ROW = 2 * DKP;                     // k and q of a token
     constexpr int NKQ = (kScanChunk * ROW + kScanThreads - 1) / kScanThreads;
+    constexpr int NP = ST / 2;                       // pairs of columns of a thread
     typedef Pack<IO, 1> P;
     __shared__ __align__(16) float kq[2][kScanChunk * ROW];
 
@@ -35,91 +36,114 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
     const int grp = (int)(bid % (unsigned)ngrp);
     bid /= (unsigned)ngrp;
     const int bh = (int)(bid % (unsigned)(a.B * a.H));
-    const int seg = (int)(bid / (unsigned)(a.B * a.H));
+    const int seg0 = (int)(bid / (unsigned)(a.B * a.H)) * (MODE == kScanBoth ? w.run : 1);
     const int b = bh / a.H, h = bh % a.H;
     const int tid = threadIdx.x;
     const int sl = tid % SL, ch = grp * CPB + tid / SL;
     const bool ok = ch < a.dv;
     const int n = seq_length(a.lengths, b, a.T);
-    const long long first = (long long)seg * w.seg;
-    const int t0 = (int)(first < n ? first : n);
-    const int t1 = (int)(first + w.seg < n ? first + w.seg : n);
+    // tokens [t0, t1), of which those below n are there
+    const long long first = (long long)seg0 * w.seg;
+    const long long last = MODE == kScanBoth ? first + (long long)w.run * w.seg : first + w.seg;
+    const int t0 = (int)(first < a.T ? first : a.T);
+    const int t1 = (int)(last < a.T ? last : a.T);
+    const int te = n < t1 ? n : t1;
 
-    const long long hc = (long long)h * a.dv + ch;               // (H,dv)
-    const long long bhc = (long long)bh * a.dv + ch;             // (B,H,dv)
-    const long long plane = (long long)a.B * a.H * a.dv * a.dk;  // one segment's states
-    const long long rows = (long long)a.B * a.H * a.dv;
+    const long long hc = (long long)h * a.dv + (ok ? ch : 0);      // (H,dv)
+    const long long bhc = (long long)bh * a.dv + (ok ? ch : 0);    // (B,H,dv)
+    const float *S0 = a.S0 ? a.S0 + bhc * a.dk : nullptr;
+    float *const ends = w.ends + bhc * w.nseg * DKP + sl * ST;     // this thread's columns, segment by segment
+    float *const steps = w.steps + bhc * w.nseg;
 
-    if (MODE == kScanEnds && seg == w.nseg - 1) {
+    if (MODE == kScanEnds && seg0 == w.nseg - 1) {
         // the last segment's end is not needed: its place keeps the initial state for the second launch,
         // which may write S_out over S0
         if (ok)
 #pragma unroll
             for (int s = 0; s < ST; ++s)
-                if (sl * ST + s < a.dk)
-                    w.ends[seg * plane + bhc * a.dk + sl * ST + s] = a.S0 ? a.S0[bhc * a.dk + sl * ST + s] : 0.f;
+                ends[(long long)seg0 * DKP + s] = S0 && sl * ST + s < a.dk ? S0[sl * ST + s] : 0.f;
         return;
     }
 
-    float A2[ST], S[ST], Pr[MODE == kScanBoth ? ST : 1], G[MODE == kScanBoth ? ST : 1];
+    f32x2 A2[NP], S[NP], Pr[MODE == kScanBoth ? NP : 1], G[MODE == kScanBoth ? NP : 1];
+    auto column = [&](const float *row, int s) { return ok && row && sl * ST + s < a.dk ? row[sl * ST + s] : 0.f; };
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-        const int c = sl * ST + s;
-        A2[s] = ok && c < a.dk ? a.A[hc * a.dk + c] * kLog2e : 0.f;
-        S[s] = 0.f;
-        if (MODE == kScanBoth) { Pr[s] = 1.f; G[s] = 0.f; }
+    for (int s = 0; s < NP; ++s) {
+        A2[s] = pack2(column(a.A + hc * a.dk, 2 * s) * kLog2e, column(a.A + hc * a.dk, 2 * s + 1) * kLog2e);
+        S[s] = 0ull;
+        if (MODE == kScanBoth) { Pr[s] = pack2(1.f, 1.f); G[s] = 0ull; }
     }
     const float bias = ok && a.delta_bias ? a.delta_bias[hc] : 0.f;
     const float skip = ok && MODE == kScanFull && a.D ? a.D[hc] : 0.f;
     const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0;
-    if (MODE == kScanFull && ok) {
-        const float *from = w.nseg > 1 ? w.ends + (long long)(w.nseg - 1) * plane : a.S0;
+    if (MODE == kScanFull) {
+        if (w.nseg == 1) {
 #pragma unroll
-        for (int s = 0; s < ST; ++s)
-            if (from && sl * ST + s < a.dk) S[s] = from[bhc * a.dk + sl * ST + s];
-        for (int j = 0; j < seg; ++j) {
-            const float sd = w.steps[j * rows + bhc];
-            const float *e = w.ends + j * plane + bhc * a.dk + sl * ST;
+            for (int s = 0; s < NP; ++s) S[s] = pack2(column(S0, 2 * s), column(S0, 2 * s + 1));
+        } else if (ok) {
 #pragma unroll
-            for (int s = 0; s < ST; ++s)
-                if (sl * ST + s < a.dk) S[s] = fmaf(fast_ex2(A2[s] * sd), S[s], e[s]);
+            for (int s = 0; s < NP; s += 2) load_pairs(ends + (long long)(w.nseg - 1) * DKP + 2 * s, S[s], S[s + 1]);
+#pragma unroll 2
+            for (int j = 0; j < seg0; ++j) {
+                const float sd = steps[j];
+                const f32x2 sd2 = pack2(sd, sd);
+#pragma unroll
+                for (int s = 0; s < NP; s += 2) {
+                    f32x2 e0, e1;
+                    load_pairs(ends + (long long)j * DKP + 2 * s, e0, e1);
+                    S[s] = fma2(ex2_2(mul2(A2[s], sd2)), S[s], e0);
+                    S[s + 1] = fma2(ex2_2(mul2(A2[s + 1], sd2)), S[s + 1], e1);
+                }
+            }
         }
     }
 
-    const IO *pv = row_of<IO>(a.v, b, h, 0) + ch;
-    const IO *pd = row_of<IO>(a.delta, b, h, 0) + ch;
-    const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, 0) + ch : nullptr;
-    const IO *pk = row_of<IO>(a.k, b, h, 0);
-    const IO *pq = row_of<IO>(a.q, b, h, 0);
-    const float *pg = MODE == kScanBoth ? row_of<float>(w.dO, b, h, 0) + ch : nullptr;
-    IO *po = MODE == kScanFull ? row_of<IO>(a.o, b, h, 0) + ch : nullptr;
+    const unsigned cu = ok ? (unsigned)ch : 0u;
+    const IO *pv = row_of<IO>(a.v, b, h, t0), *pd = row_of<IO>(a.delta, b, h, t0);
+    const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, t0) : nullptr;
+    const IO *pk = row_of<IO>(a.k, b, h, 0), *pq = row_of<IO>(a.q, b, h, 0);
+    const float *pg = MODE == kScanBoth ? row_of<float>(w.dO, b, h, t0) : nullptr;
+    IO *po = MODE == kScanFull ? row_of<IO>(a.o, b, h, t0) : nullptr;
 
     typename P::raw rv[kScanChunk], rd[kScanChunk], rz[kScanChunk], rkq[NKQ];
     float rg[MODE == kScanBoth ? kScanChunk : 1];
+    // loads of the chunk at t, and the row pointers on to the next one
     auto fetch = [&](int t) {
+        const bool whole = t + kScanChunk <= te;
 #pragma unroll
         for (int j = 0; j < kScanChunk; ++j) {
-            const bool in = ok && t + j < t1;
-            rv[j] = in ? P::ld(pv + (t + j) * a.v.st) : P::zero();
-            rd[j] = in ? P::ld(pd + (t + j) * a.delta.st) : P::zero();
-            if (MODE != kScanEnds) rz[j] = in && pz ? P::ld(pz + (t + j) * a.z.st) : P::zero();
-            if (MODE == kScanBoth) rg[j] = in ? pg[(t + j) * w.dO.st] : 0.f;
+            const bool in = whole || t + j < te;
+            rv[j] = P::zero();
+            rd[j] = P::zero();
+            if (MODE != kScanEnds) rz[j] = P::zero();
+            if (MODE == kScanBoth) rg[j] = 0.f;
+            if (in) {
+                rv[j] = P::ld(pv + cu);
+                rd[j] = P::ld(pd + cu);
+                if (MODE != kScanEnds && pz) rz[j] = P::ld(pz + cu);
+                if (MODE == kScanBoth) rg[j] = pg[cu];
+            }
+            pv += a.v.st;
+            pd += a.delta.st;
+            if (MODE != kScanEnds && pz) pz += a.z.st;
+            if (MODE == kScanBoth) pg += w.dO.st;
         }
 #pragma unroll
         for (int m = 0; m < NKQ; ++m) {
             const int e = tid + m * kScanThreads, j = e / ROW, c = e % DKP;
             const bool isq = e % ROW >= DKP;
             rkq[m] = P::zero();
-            if (e < kScanChunk * ROW && t + j < t1 && c < a.dk && !(MODE == kScanEnds && isq))
+            if (e < kScanChunk * ROW && t + j < te && c < a.dk && !(MODE == kScanEnds && isq))
                 rkq[m] = isq ? P::ld(pq + (t + j) * a.q.st + c) : P::ld(pk + (t + j) * a.k.st + c);
         }
     };
 
     float sum = 0.f;
+    int seg = seg0, left = w.seg;   // kScanBoth: the segment being walked and its tokens to come
     fetch(t0);
     int buf = 0;
-    for (int t = t0; t < t1; t += kScanChunk, buf ^= 1) {
-        float dt[kScanChunk], dtv[kScanChunk], v[kScanChunk], z[kScanChunk], g[kScanChunk];
+    for (int t = t0; t < (MODE == kScanBoth ? t1 : te); t += kScanChunk, buf ^= 1) {
+        float dt[kScanChunk], v[kScanChunk], z[kScanChunk], g[kScanChunk];
 #pragma unroll
         for (int m = 0; m < NKQ; ++m) {
             const int e = tid + m * kScanThreads;
@@ -134,62 +158,99 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
             v[j] = x[0];
             P::cvt(rd[j], x);
             const float raw = x[0] + bias;
-            dt[j] = ok && t + j < t1 ? (soft ? softplus(raw) : raw) : 0.f;   // 0 behind the end: the state stays
-            dtv[j] = dt[j] * v[j];
+            dt[j] = soft ? softplus(raw) : raw;
             if (MODE != kScanEnds) {
                 P::cvt(rz[j], x);
                 z[j] = x[0];
             }
-            if (MODE == kScanBoth) g[j] = pz ? rg[j] * silu(z[j]) : rg[j];
-            if (MODE != kScanFull) sum += dt[j];
+            g[j] = MODE == kScanBoth ? (pz ? rg[j] * silu(z[j]) : rg[j]) : 0.f;
         }
-        if (t + kScanChunk < t1) fetch(t + kScanChunk);
+        if (t + kScanChunk > te) {   // behind the end the step is 0, the state stays, and nothing flows back
+#pragma unroll
+            for (int j = 0; j < kScanChunk; ++j)
+                if (t + j >= te) dt[j] = v[j] = g[j] = 0.f;
+        }
+        if (t + kScanChunk < te) fetch(t + kScanChunk);
         __syncthreads();   // the chunk is staged; the other buffer was last read before this barrier
+        const bool whole = t + kScanChunk <= te;
 #pragma unroll
         for (int j = 0; j < kScanChunk; ++j) {
-            const float4 *k4 = reinterpret_cast<const float4 *>(&kq[buf][j * ROW + sl * ST]);
-            const float4 *q4 = reinterpret_cast<const float4 *>(&kq[buf][j * ROW + DKP + sl * ST]);
-            float y = 0.f;
+            const float *k4 = &kq[buf][j * ROW + sl * ST];
+            const float *q4 = &kq[buf][j * ROW + DKP + sl * ST];
+            const f32x2 dt2 = pack2(dt[j], dt[j]);
+            const float b1 = dt[j] * v[j];
+            const f32x2 b2 = pack2(b1, b1);
+            f32x2 y2 = 0ull, g2 = 0ull;
+            if (MODE == kScanBoth) g2 = pack2(g[j], g[j]);
+            if (MODE != kScanFull) sum += dt[j];
 #pragma unroll
-            for (int s4 = 0; s4 < ST / 4; ++s4) {
-                const float4 kk = k4[s4];
-                float4 qq = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (MODE != kScanEnds) qq = q4[s4];
-                const float kx[4] = {kk.x, kk.y, kk.z, kk.w}, qx[4] = {qq.x, qq.y, qq.z, qq.w};
+            for (int s = 0; s < NP; s += 2) {
+                f32x2 kk[2], qq[2];
+                load_pairs(k4 + 2 * s, kk[0], kk[1]);
+                if (MODE != kScanEnds) load_pairs(q4 + 2 * s, qq[0], qq[1]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int s = s4 * 4 + r;
-                    const float e = fast_ex2(dt[j] * A2[s]);
-                    S[s] = fmaf(e, S[s], dtv[j] * kx[r]);
-                    if (MODE == kScanFull) y = fmaf(S[s], qx[r], y);
+                for (int r = 0; r < 2; ++r) {
+                    const f32x2 e = ex2_2(mul2(dt2, A2[s + r]));
+                    S[s + r] = fma2(e, S[s + r], mul2(b2, kk[r]));
+                    if (MODE == kScanFull) y2 = fma2(S[s + r], qq[r], y2);
                     if (MODE == kScanBoth) {
-                        Pr[s] *= e;
-                        G[s] = fmaf(Pr[s], g[j] * qx[r], G[s]);
+                        Pr[s + r] = mul2(Pr[s + r], e);
+                        G[s + r] = fma2(Pr[s + r], mul2(g2, qq[r]), G[s + r]);
                     }
                 }
             }
             if (MODE == kScanFull) {
+                float y = sum2(y2);
 #pragma unroll
                 for (int m = 1; m < SL; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
                 y = fmaf(skip, v[j], y);
                 if (pz) y *= silu(z[j]);
-                if (ok && sl == 0 && t + j < t1) {
+                if (ok && sl == 0 && (whole || t + j < te)) {
                     const float out[1] = {y};
-                    P::st(po + (t + j) * a.o.st, out);
+                    P::st(po + cu, out);
+                }
+                po += a.o.st;
+            }
+        }
+        if (MODE == kScanBoth) {
+            left -= kScanChunk;
+            if (left == 0 || t + kScanChunk >= t1) {   // the segment's end: hand it over, start the next from zero
+                if (ok) {
+                    float *const to = ends + (long long)seg * DKP, *const tg = w.grads + (bhc * w.nseg + seg) * DKP + sl * ST;
+#pragma unroll
+                    for (int s = 0; s < NP; s += 2) {
+                        store_pairs(to + 2 * s, S[s], S[s + 1]);
+                        store_pairs(tg + 2 * s, G[s], G[s + 1]);
+                    }
+                    if (sl == 0) steps[seg] = sum;
+                }
+                ++seg;
+                left = w.seg;
+                sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < NP; ++s) {
+                    S[s] = 0ull;
+                    G[s] = 0ull;
+                    Pr[s] = pack2(1.f, 1.f);
                 }
             }
         }
     }
-    if (!ok) return;
-    float *to = MODE == kScanFull ? (seg == w.nseg - 1 ? a.S_out : nullptr) : w.ends + seg * plane;
+    if (MODE == kScanBoth || !ok) return;
+    if (MODE == kScanEnds) {
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-        const int c = sl * ST + s;
-        if (c >= a.dk) continue;
-        if (to) to[bhc * a.dk + c] = S[s];
-        if (MODE == kScanBoth) w.grads[seg * plane + bhc * a.dk + c] = G[s];
+        for (int s = 0; s < NP; s += 2) store_pairs(ends + (long long)seg0 * DKP + 2 * s, S[s], S[s + 1]);
+        if (sl == 0) steps[seg0] = sum;
+    } else if (a.S_out && seg0 == w.nseg - 1) {
+        float *to = a.S_out + bhc * a.dk;
+#pragma unroll
+        for (int s = 0; s < NP; ++s) {
+            float lo, hi;
+            unpack2(S[s], lo, hi);
+            if (sl * ST + 2 * s < a.dk) to[sl * ST + 2 * s] = lo;
+            if (sl * ST + 2 * s + 1 < a.dk) to[sl * ST + 2 * s + 1] = hi;
+        }
     }
-    if (MODE != kScanFull && sl == 0) w.steps[seg * rows + bhc] = sum;
 }
 
 // One token. A channel's row of the state is read and written by G lanes, four columns each, so the
@@ -276,7 +337,8 @@ template <typename IO, int ST, int SL>
 cudaError_t scan_pass_t(int mode, const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
     const int cpb = kScanThreads / SL;
     const int ngrp = (a.dv + cpb - 1) / cpb;
-    const long long blocks = (long long)ngrp * a.B * a.H * w.nseg;
+    const int runs = mode == kScanBoth ? (w.nseg + w.run - 1) / w.run : w.nseg;
+    const long long blocks = (long long)ngrp * a.B * a.H * runs;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     if (mode == kScanFull) scan_kernel<IO, ST, SL, kScanFull><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
     else if (mode == kScanEnds) scan_kernel<IO, ST, SL, kScanEnds><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
@@ -341,7 +403,7 @@ ScanPlan scan_plan(const falcon_scan_args_t &a, int num_sms) {
     seg = (seg + kScanChunk - 1) / kScanChunk * kScanChunk;
     p.seg = (int)seg;
     p.nseg = (int)((a.T + seg - 1) / seg);
-    p.bytes = (size_t)p.nseg * bh * a.dv * (a.dk + 1) * sizeof(float);
+    p.bytes = (size_t)p.nseg * bh * a.dv * (scan_cols(a.dk) + 1) * sizeof(float);
     return p;
 }
 
@@ -352,7 +414,7 @@ cudaError_t launch_scan_fwd(const falcon_scan_args_t &a, const ScanPlan &plan, f
     w.nseg = plan.nseg;
     if (plan.nseg > 1) {
         w.ends = ws;
-        w.steps = ws + (size_t)plan.nseg * a.B * a.H * a.dv * a.dk;
+        w.steps = ws + (size_t)plan.nseg * a.B * a.H * a.dv * scan_cols(a.dk);
         const cudaError_t e = launch_scan_pass(kScanEnds, a, w, s);
         if (e != cudaSuccess) return e;
     }
