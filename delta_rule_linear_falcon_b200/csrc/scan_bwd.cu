@@ -36,8 +36,8 @@ template <int SL> struct BwdShape {
     static constexpr int kChan = kSeg * kCh;             // one array over (token, channel)
     static constexpr int kKq = kSeg * kCols;             // k or q
     static constexpr int kRed = kWarps * kSeg * kCols;   // a warp's part of dq or dk
-    static constexpr int kStart = kNSub * 16 * kThreads;
-    static constexpr size_t kBytes = sizeof(float) * (4 * kChan + 2 * kKq + 2 * kRed + kStart);
+    static constexpr int kStart = (kNSub - 1) * 16 * kThreads;
+    static constexpr size_t kBytes = sizeof(float) * (4 * kChan + 4 * kKq + 2 * kRed + kStart);
 };
 
 struct ScanBwdWork {
@@ -100,17 +100,18 @@ __global__ void __launch_bounds__(256) scan_join_kernel(falcon_scan_args_t a, Sc
 }
 
 template <typename IO, int SL>
-__global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g,
-                                                                          ScanBwdWork w, int ngrp) {
+__global__ void __launch_bounds__(BwdShape<SL>::kThreads, BwdShape<SL>::kWarps == 4 ? 3 : 1)
+scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int ngrp) {
     typedef BwdShape<SL> Sh;
+    typedef Pack<IO, 1> P;
     constexpr int NT = Sh::kThreads, CH = Sh::kCh, COLS = Sh::kCols, CL = 32 / SL;
     extern __shared__ __align__(16) float sm[];
     float *sDt = sm;                    // [token][channel]: dt;  after its token: sum_c G k
     float *sDv = sDt + Sh::kChan;       // dt v;                  after its token: sum_c A W
     float *sDy = sDv + Sh::kChan;       // dy
     float *sY = sDy + Sh::kChan;        // sum_c S q
-    float *sK = sY + Sh::kChan, *sQ = sK + Sh::kKq;
-    float *sDq = sQ + Sh::kKq, *sDk = sDq + Sh::kRed;   // [warp][token][column]
+    float *sK = sY + Sh::kChan, *sQ = sK + 2 * Sh::kKq;     // [token][column], every value twice: a pair's factor
+    float *sDq = sQ + 2 * Sh::kKq, *sDk = sDq + Sh::kRed;   // [warp][token][column]
     float *start = sDk + Sh::kRed;      // [sub][4][thread] float4: the state before a sub-segment
 
     unsigned bid = blockIdx.x;
@@ -125,24 +126,22 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
     const int c00 = grp * CH;
     const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0;
 
-    const IO *pv = row_of<IO>(a.v, b, h, 0), *pd = row_of<IO>(a.delta, b, h, 0);
-    const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, 0) : nullptr;
-    const IO *pk = row_of<IO>(a.k, b, h, 0), *pq = row_of<IO>(a.q, b, h, 0);
-    const float *pg = row_of<float>(g.dO, b, h, 0);
-
-    // this thread's 4 channels x 4 columns, as pairs of columns
+    // this thread's 4 channels x 4 columns, as pairs of channels: factors of a channel (dt, dt v, dy) are pairs as
+    // they lie, factors of a column (k, q) pairs of one value, and sums over columns need no last addition
     const int lc = warp * Sh::kChWarp + cl * 4;   // first channel in the block
-    f32x2 A2[4][2], S[4][2], G[4][2], dA[4][2];
+    f32x2 A2[2][4], S[2][4], G[2][4], dA[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int ch = c00 + lc + i;
-        const float *row = a.A + ((long long)h * a.dv + ch) * a.dk;
+    for (int s = 0; s < 4; ++s) {
+        const int c = sl * 4 + s;
+        float x[4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int c = sl * 4 + 2 * s;
-            A2[i][s] = pack2(ch < a.dv && c < a.dk ? row[c] * kLog2e : 0.f, ch < a.dv && c + 1 < a.dk ? row[c + 1] * kLog2e : 0.f);
-            dA[i][s] = 0ull;
+        for (int i = 0; i < 4; ++i) {
+            const int ch = c00 + lc + i;
+            x[i] = ch < a.dv && c < a.dk ? a.A[((long long)h * a.dv + ch) * a.dk + c] * kLog2e : 0.f;
         }
+        A2[0][s] = pack2(x[0], x[1]);
+        A2[1][s] = pack2(x[2], x[3]);
+        dA[0][s] = dA[1][s] = 0ull;
     }
     float dd[Sh::kPer], db[Sh::kPer], skip[Sh::kPer], bias[Sh::kPer];   // of the channels tid, tid + NT, ..
 #pragma unroll
@@ -154,91 +153,121 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
         bias[m] = ok && a.delta_bias ? a.delta_bias[(long long)h * a.dv + ch] : 0.f;
     }
 
-    auto keep = [&](int slot) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) store_pairs(start + ((slot * 4 + i) * NT + tid) * 4, S[i][0], S[i][1]);
-    };
-    auto four = [](const float *p, float (&x)[4]) {
-        const float4 f = *reinterpret_cast<const float4 *>(p);
-        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-    };
     auto advance = [&](int t) {   // S_{t-1} -> S_t
-        float dt[4], dtv[4];
-        f32x2 k[2];
-        four(sDt + t * CH + lc, dt);
-        four(sDv + t * CH + lc, dtv);
-        load_pairs(sK + t * COLS + sl * 4, k[0], k[1]);
+        f32x2 dt[2], dtv[2], k[4];
+        load_pairs(sDt + t * CH + lc, dt[0], dt[1]);
+        load_pairs(sDv + t * CH + lc, dtv[0], dtv[1]);
+        load_pairs(sK + (t * COLS + sl * 4) * 2, k[0], k[1]);
+        load_pairs(sK + (t * COLS + sl * 4) * 2 + 4, k[2], k[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x2 dt2 = pack2(dt[i], dt[i]), b2 = pack2(dtv[i], dtv[i]);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) S[i][s] = fma2(ex2_2(mul2(dt2, A2[i][s])), S[i][s], mul2(b2, k[s]));
-        }
+            for (int s = 0; s < 4; ++s) S[i][s] = fma2(ex2_2(mul2(dt[i], A2[i][s])), S[i][s], mul2(dtv[i], k[s]));
     };
-    bool write;
 
     const int seg_end = min((runi + 1) * w.run, w.nseg);
 #pragma unroll 1
     for (int seg = runi * w.run; seg < seg_end; ++seg) {
         const int t0 = seg * kSeg;
-        // ---- the segment's inputs; thread tid stages the channels whose gradients it forms
+        const int here = min(max(n - t0, 0), kSeg), rows = min(a.T - t0, kSeg);   // tokens of the sequence; of the arrays
+        // ---- the segment's states (one load per channel), then its inputs
+        {
+            f32x2 x[4][2], y[4][2];
 #pragma unroll
-        for (int m = 0; m < Sh::kPer; ++m) {
-            const int cc = tid + m * NT, ch = c00 + cc;
-            if (cc >= CH) continue;
-#pragma unroll 8
-            for (int j = 0; j < kSeg; ++j) {
-                const int t = t0 + j;
-                float dt = 0.f, dtv = 0.f, dy = 0.f;
-                if (t < n && ch < a.dv) {
-                    dt = Io<IO>::ld(pd, t * a.delta.st + ch) + bias[m];
-                    if (soft) dt = softplus(dt);
-                    dtv = dt * Io<IO>::ld(pv, t * a.v.st + ch);
-                    dy = pg[t * g.dO.st + ch];
-                    if (pz) dy *= silu(Io<IO>::ld(pz, t * a.z.st + ch));
+            for (int i = 0; i < 4; ++i) {
+                const int ch = c00 + lc + i;
+                x[i][0] = x[i][1] = y[i][0] = y[i][1] = 0ull;
+                if (ch < a.dv) {
+                    const long long at = (((long long)bh * a.dv + ch) * w.nseg + seg) * COLS + sl * 4;
+                    load_pairs(w.ends + at, x[i][0], x[i][1]);
+                    load_pairs(w.grads + at, y[i][0], y[i][1]);
                 }
-                sDt[j * CH + cc] = dt;
-                sDv[j * CH + cc] = dtv;
-                sDy[j * CH + cc] = dy;
             }
-        }
-        for (int idx = tid; idx < Sh::kKq; idx += NT) {
-            const int t = t0 + idx / COLS, c = idx % COLS;
-            const bool in = t < n && c < a.dk;
-            sK[idx] = in ? Io<IO>::ld(pk, t * a.k.st + c) : 0.f;
-            sQ[idx] = in ? Io<IO>::ld(pq, t * a.q.st + c) : 0.f;
-        }
+            const IO *pk = row_of<IO>(a.k, b, h, t0), *pq = row_of<IO>(a.q, b, h, t0);
+            for (int idx = tid; idx < Sh::kKq; idx += NT) {
+                const int j = idx / COLS, c = idx % COLS;
+                const bool in = j < here && c < a.dk;
+                const float kk = in ? Io<IO>::ld(pk, j * a.k.st + c) : 0.f;
+                const float qq = in ? Io<IO>::ld(pq, j * a.q.st + c) : 0.f;
+                reinterpret_cast<float2 *>(sK)[idx] = make_float2(kk, kk);
+                reinterpret_cast<float2 *>(sQ)[idx] = make_float2(qq, qq);
+            }
+            // thread tid stages the channels whose gradients it forms
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ch = c00 + lc + i;
-            S[i][0] = S[i][1] = G[i][0] = G[i][1] = 0ull;
-            if (ch < a.dv) {
-                const long long at = (((long long)bh * a.dv + ch) * w.nseg + seg) * COLS + sl * 4;
-                load_pairs(w.ends + at, S[i][0], S[i][1]);
-                load_pairs(w.grads + at, G[i][0], G[i][1]);
+            for (int m = 0; m < Sh::kPer; ++m) {
+                const int cc = tid + m * NT, ch = c00 + cc;
+                if (cc >= CH) continue;
+                const bool ok = ch < a.dv;
+                const IO *pv = row_of<IO>(a.v, b, h, t0) + ch, *pd = row_of<IO>(a.delta, b, h, t0) + ch;
+                const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, t0) + ch : nullptr;
+                const float *pg = row_of<float>(g.dO, b, h, t0) + ch;
+                constexpr int U = 8;
+#pragma unroll 1
+                for (int j0 = 0; j0 < kSeg; j0 += U) {
+                    typename P::raw rv[U], rd[U], rz[U];
+                    float rg[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool in = ok && j0 + u < here;
+                        rv[u] = rd[u] = rz[u] = P::zero();
+                        rg[u] = 0.f;
+                        if (in) {
+                            rv[u] = P::ld(pv);
+                            rd[u] = P::ld(pd);
+                            if (pz) rz[u] = P::ld(pz);
+                            rg[u] = *pg;
+                        }
+                        pv += a.v.st;
+                        pd += a.delta.st;
+                        if (pz) pz += a.z.st;
+                        pg += g.dO.st;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int at = (j0 + u) * CH + cc;
+                        float dt = Io<IO>::cvt(rd[u]) + bias[m];
+                        if (soft) dt = softplus(dt);
+                        if (!(ok && j0 + u < here)) dt = 0.f;
+                        sDt[at] = dt;
+                        sDv[at] = dt * Io<IO>::cvt(rv[u]);
+                        sDy[at] = pz ? rg[u] * silu(Io<IO>::cvt(rz[u])) : rg[u];
+                    }
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    float p0, p1, r0, r1;
+                    unpack2(x[2 * i][s], p0, p1);
+                    unpack2(x[2 * i + 1][s], r0, r1);
+                    S[i][2 * s] = pack2(p0, r0);
+                    S[i][2 * s + 1] = pack2(p1, r1);
+                    unpack2(y[2 * i][s], p0, p1);
+                    unpack2(y[2 * i + 1][s], r0, r1);
+                    G[i][2 * s] = pack2(p0, r0);
+                    G[i][2 * s + 1] = pack2(p1, r1);
+                }
         }
         __syncthreads();
 
-        // ---- forward
-#pragma unroll 1
-        for (int t = 0; t < kSeg; ++t) {
-            if (t % kSub == 0) keep(t / kSub);
-            advance(t);
-            f32x2 q[2], dq2[2];
-            float dy[4], y[4], dq[4];
-            load_pairs(sQ + t * COLS + sl * 4, q[0], q[1]);
-            four(sDy + t * CH + lc, dy);
-            dq2[0] = dq2[1] = 0ull;
+        // ---- forward, all but the last sub-segment
+        auto outputs = [&](int t) {   // y_t and this warp's part of dq_t from S_t
+            f32x2 q[4], dy[2];
+            float y[4], dq[4];
+            load_pairs(sQ + (t * COLS + sl * 4) * 2, q[0], q[1]);
+            load_pairs(sQ + (t * COLS + sl * 4) * 2 + 4, q[2], q[3]);
+            load_pairs(sDy + t * CH + lc, dy[0], dy[1]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x2 dy2 = pack2(dy[i], dy[i]);
-                y[i] = sum2(fma2(S[i][1], q[1], mul2(S[i][0], q[0])));
-                dq2[0] = fma2(S[i][0], dy2, dq2[0]);
-                dq2[1] = fma2(S[i][1], dy2, dq2[1]);
+            for (int i = 0; i < 2; ++i) {
+                f32x2 y2 = mul2(S[i][0], q[0]);
+#pragma unroll
+                for (int s = 1; s < 4; ++s) y2 = fma2(S[i][s], q[s], y2);
+                unpack2(y2, y[2 * i], y[2 * i + 1]);
             }
-            unpack2(dq2[0], dq[0], dq[1]);
-            unpack2(dq2[1], dq[2], dq[3]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) dq[s] = sum2(fma2(S[1][s], dy[1], mul2(S[0][s], dy[0])));
+            bool write;
             const int iy = lanes_sum<4, SL, 1>(y, lane, write);
             if (write)
 #pragma unroll
@@ -247,53 +276,71 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
             if (write)
 #pragma unroll
                 for (int s = 0; s < (CL >= 4 ? 1 : 4 / CL); ++s) sDq[(warp * kSeg + t) * COLS + sl * 4 + iq + s] = dq[s];
+        };
+#pragma unroll 1
+        for (int t = 0; t < kSeg - kSub; ++t) {
+            if (t % kSub == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_pairs(start + ((t / kSub * 4 + i) * NT + tid) * 4, S[i / 2][i % 2 * 2], S[i / 2][i % 2 * 2 + 1]);
+            }
+            advance(t);
+            outputs(t);
         }
 
-        // ---- backward
+        // ---- sub-segment by sub-segment from the end: the states before its tokens, then backward
 #pragma unroll 1
         for (int sub = kNSub - 1; sub >= 0; --sub) {
-            f32x2 before[kSub][4][2];   // the state before each token
+            f32x2 before[kSub][2][4];
+            const bool last = sub == kNSub - 1;   // its forward pass is still to come
+            if (!last) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_pairs(start + ((sub * 4 + i) * NT + tid) * 4, S[i][0], S[i][1]);
+                for (int i = 0; i < 4; ++i)
+                    load_pairs(start + ((sub * 4 + i) * NT + tid) * 4, S[i / 2][i % 2 * 2], S[i / 2][i % 2 * 2 + 1]);
+            }
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    before[j][i][0] = S[i][0];
-                    before[j][i][1] = S[i][1];
-                }
-                if (j < kSub - 1) advance(sub * kSub + j);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) before[j][i][s] = S[i][s];
+                if (j < kSub - 1 || last) advance(sub * kSub + j);
+                if (last) outputs(sub * kSub + j);
             }
 #pragma unroll
             for (int j = kSub - 1; j >= 0; --j) {
                 const int t = sub * kSub + j;
-                float dt[4], dtv[4], dy[4], dk[4], ch[8];
-                f32x2 k[2], q[2], dk2[2];
-                four(sDt + t * CH + lc, dt);
-                four(sDv + t * CH + lc, dtv);
-                four(sDy + t * CH + lc, dy);
-                load_pairs(sK + t * COLS + sl * 4, k[0], k[1]);
-                load_pairs(sQ + t * COLS + sl * 4, q[0], q[1]);
-                dk2[0] = dk2[1] = 0ull;
+                f32x2 dt[2], dtv[2], dy[2], k[4], q[4];
+                float dk[4], ch[8];
+                bool write;
+                load_pairs(sDt + t * CH + lc, dt[0], dt[1]);
+                load_pairs(sDv + t * CH + lc, dtv[0], dtv[1]);
+                load_pairs(sDy + t * CH + lc, dy[0], dy[1]);
+                load_pairs(sK + (t * COLS + sl * 4) * 2, k[0], k[1]);
+                load_pairs(sK + (t * COLS + sl * 4) * 2 + 4, k[2], k[3]);
+                load_pairs(sQ + (t * COLS + sl * 4) * 2, q[0], q[1]);
+                load_pairs(sQ + (t * COLS + sl * 4) * 2 + 4, q[2], q[3]);
+                f32x2 gk[2] = {0ull, 0ull}, aw[2] = {0ull, 0ull};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x2 dt2 = pack2(dt[i], dt[i]), b2 = pack2(dtv[i], dtv[i]), dy2 = pack2(dy[i], dy[i]);
-                    f32x2 gk = 0ull, aw = 0ull;
+                for (int s = 0; s < 4; ++s) {
+                    f32x2 dk2 = 0ull;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const f32x2 gs = fma2(dy2, q[s], G[i][s]);
-                        gk = fma2(gs, k[s], gk);
-                        dk2[s] = fma2(gs, b2, dk2[s]);
-                        G[i][s] = mul2(gs, ex2_2(mul2(dt2, A2[i][s])));
+                    for (int i = 0; i < 2; ++i) {
+                        const f32x2 gs = fma2(dy[i], q[s], G[i][s]);
+                        gk[i] = fma2(gs, k[s], gk[i]);
+                        dk2 = fma2(gs, dtv[i], dk2);
+                        G[i][s] = mul2(gs, ex2_2(mul2(dt[i], A2[i][s])));
                         const f32x2 W = mul2(G[i][s], before[j][i][s]);
-                        aw = fma2(A2[i][s], W, aw);
-                        dA[i][s] = fma2(dt2, W, dA[i][s]);
+                        aw[i] = fma2(A2[i][s], W, aw[i]);
+                        dA[i][s] = fma2(dt[i], W, dA[i][s]);
                     }
-                    ch[i] = sum2(gk);
-                    ch[4 + i] = sum2(aw);
+                    dk[s] = sum2(dk2);
                 }
-                unpack2(dk2[0], dk[0], dk[1]);
-                unpack2(dk2[1], dk[2], dk[3]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    unpack2(gk[i], ch[2 * i], ch[2 * i + 1]);
+                    unpack2(aw[i], ch[4 + 2 * i], ch[5 + 2 * i]);
+                }
                 const int ik = lanes_sum<4, CL, SL>(dk, lane, write);
                 if (write)
 #pragma unroll
@@ -316,35 +363,65 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
         for (int m = 0; m < Sh::kPer; ++m) {
             const int cc = tid + m * NT, ch = c00 + cc;
             if (cc >= CH || ch >= a.dv) continue;
-#pragma unroll 8
-            for (int j = 0; j < kSeg; ++j) {
-                const int t = t0 + j;
-                if (t >= a.T) break;
-                float dv = 0.f, ddl = 0.f, dz = 0.f;
-                if (t < n) {
-                    const float gk = sDt[j * CH + cc], aw = sDv[j * CH + cc], dy = sDy[j * CH + cc];
-                    const float raw = Io<IO>::ld(pd, t * a.delta.st + ch) + bias[m];
-                    const float v = Io<IO>::ld(pv, t * a.v.st + ch);
-                    const float dt = soft ? softplus(raw) : raw;
-                    dv = fmaf(dt, gk, skip[m] * dy);
-                    ddl = fmaf(v, gk, aw);
-                    if (soft) ddl *= sigmoid(raw);
-                    if (pz) {
-                        const float z = Io<IO>::ld(pz, t * a.z.st + ch);
-                        dz = pg[t * g.dO.st + ch] * fmaf(skip[m], v, sY[j * CH + cc]) * silu_grad(z);
+            const IO *pv = row_of<IO>(a.v, b, h, t0) + ch, *pd = row_of<IO>(a.delta, b, h, t0) + ch;
+            const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, t0) + ch : nullptr;
+            const float *pg = row_of<float>(g.dO, b, h, t0) + ch;
+            float *ov = row_of<float>(g.dv, b, h, t0) + ch, *od = row_of<float>(g.ddelta, b, h, t0) + ch;
+            float *oz = pz && g.dz.p ? row_of<float>(g.dz, b, h, t0) + ch : nullptr;
+            constexpr int U = 8;
+#pragma unroll 1
+            for (int j0 = 0; j0 < rows; j0 += U) {
+                typename P::raw rv[U], rd[U], rz[U];
+                float rg[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    rv[u] = rd[u] = rz[u] = P::zero();
+                    rg[u] = 0.f;
+                    if (j0 + u < here) {
+                        rv[u] = P::ld(pv);
+                        rd[u] = P::ld(pd);
+                        if (oz) {
+                            rz[u] = P::ld(pz);
+                            rg[u] = *pg;
+                        }
                     }
-                    dd[m] = fmaf(dy, v, dd[m]);
-                    db[m] += ddl;
+                    pv += a.v.st;
+                    pd += a.delta.st;
+                    if (oz) {
+                        pz += a.z.st;
+                        pg += g.dO.st;
+                    }
                 }
-                row_of<float>(g.dv, b, h, t)[ch] = dv;
-                row_of<float>(g.ddelta, b, h, t)[ch] = ddl;
-                if (pz && g.dz.p) row_of<float>(g.dz, b, h, t)[ch] = dz;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int at = (j0 + u) * CH + cc;
+                    if (j0 + u < rows) {
+                        float dv = 0.f, ddl = 0.f, dz = 0.f;
+                        if (j0 + u < here) {
+                            const float gk = sDt[at], aw = sDv[at], dy = sDy[at];
+                            const float raw = Io<IO>::cvt(rd[u]) + bias[m], v = Io<IO>::cvt(rv[u]);
+                            const float dt = soft ? softplus(raw) : raw;
+                            dv = fmaf(dt, gk, skip[m] * dy);
+                            ddl = fmaf(v, gk, aw);
+                            if (soft) ddl *= sigmoid(raw);
+                            if (oz) dz = rg[u] * fmaf(skip[m], v, sY[at]) * silu_grad(Io<IO>::cvt(rz[u]));
+                            dd[m] = fmaf(dy, v, dd[m]);
+                            db[m] += ddl;
+                        }
+                        *ov = dv;
+                        *od = ddl;
+                        if (oz) *oz = dz;
+                    }
+                    ov += g.dv.st;
+                    od += g.ddelta.st;
+                    if (oz) oz += g.dz.st;
+                }
             }
         }
         // ---- dq and dk: the warps' parts
         for (int idx = tid; idx < Sh::kKq; idx += NT) {
-            const int j = idx / COLS, c = idx % COLS, t = t0 + j;
-            if (t >= a.T || c >= a.dk) continue;
+            const int j = idx / COLS, c = idx % COLS;
+            if (j >= rows || c >= a.dk) continue;
             float dq = 0.f, dk = 0.f;
 #pragma unroll
             for (int x = 0; x < Sh::kWarps; ++x) {
@@ -352,11 +429,11 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
                 dk += sDk[(x * kSeg + j) * COLS + c];
             }
             if (ngrp == 1) {
-                row_of<float>(g.dq, b, h, t)[c] = dq;
-                row_of<float>(g.dk, b, h, t)[c] = dk;
+                row_of<float>(g.dq, b, h, t0 + j)[c] = dq;
+                row_of<float>(g.dk, b, h, t0 + j)[c] = dk;
             } else {
                 const long long part = (long long)a.B * a.H * a.T * a.dk;
-                const long long at = grp * part + ((long long)bh * a.T + t) * a.dk + c;
+                const long long at = grp * part + ((long long)bh * a.T + t0 + j) * a.dk + c;
                 w.qk[at] = dq;
                 w.qk[ngrp * part + at] = dk;
             }
@@ -366,15 +443,15 @@ __global__ void __launch_bounds__(BwdShape<SL>::kThreads, 3) scan_bwd_kernel(fal
     // ---- this block's parts of the parameters' gradients
     const long long part = (long long)runi * a.B + b, HV = (long long)a.H * a.dv;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int ch = c00 + lc + i, c = sl * 4 + 2 * s;
+        for (int s = 0; s < 4; ++s) {
+            const int ch = c00 + lc + 2 * i, c = sl * 4 + s;
             float lo, hi;
             unpack2(dA[i][s], lo, hi);
             float *to = w.dA + (part * HV + (long long)h * a.dv + ch) * a.dk + c;
             if (ch < a.dv && c < a.dk) to[0] = lo;
-            if (ch < a.dv && c + 1 < a.dk) to[1] = hi;
+            if (ch + 1 < a.dv && c < a.dk) to[a.dk] = hi;
         }
 #pragma unroll
     for (int m = 0; m < Sh::kPer; ++m) {
