@@ -282,7 +282,7 @@ falcon_status_t falcon_qknorm_fwd(const falcon_qknorm_args_t *a, falcon_stream_t
     if ((long long)a->B * a->T * (a->Hq + a->Hk) == 0) return FALCON_OK;
     int sms = 0;
     FALCON_TRY(device(&sms));
-    return status_of(launch_qknorm_fwd(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(launch_qknorm_fwd(*a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t falcon_qknorm_bwd_workspace_size(const falcon_qknorm_args_t *a) {
@@ -302,7 +302,7 @@ falcon_status_t falcon_qknorm_bwd(const falcon_qknorm_args_t *a, const falcon_qk
     if (g->dwq || g->dwk) FALCON_TRY(check_workspace(workspace, workspace_bytes, qknorm_bwd_workspace(*a)));
     int sms = 0;
     FALCON_TRY(device(&sms));
-    return status_of(launch_qknorm_bwd(*a, *g, static_cast<float *>(workspace), sms, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(launch_qknorm_bwd(*a, *g, static_cast<float *>(workspace), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -3,9 +3,12 @@
 //
 // Forward: 2 K flops for an element read once and written once, so the kernel is bound by HBM. A thread
 // owns V channels (16 bytes of them where pointers, strides and d allow it, else one channel) and walks
-// a run of tokens with the last K - 1 inputs in registers; four tokens' loads are in flight at a time.
-// Neighbouring threads own neighbouring channels, so every access of a warp is whole lines, whichever of
-// token-major and head-major the two views are. A run re-reads its K - 1 first inputs (from L2).
+// a run of tokens with the last K - 1 inputs in registers. Neighbouring threads own neighbouring channels,
+// so every access of a warp is whole lines, whichever of token-major and head-major the two views are.
+// The inputs come ahead of their use through a ring in shared memory (kStages batches of kConvBatch tokens,
+// asynchronous copies into places that only the copying thread reads, so no barrier): bytes in flight cost no
+// registers. One channel a thread (V = 1): a batch's loads are in flight together. A run re-reads its K - 1
+// first inputs (from L2).
 // Backward: the same walk with a second window, of dp: step t needs x_{t-K+1..t} for p_t and act', adds
 // dp_t x to dw, and emits dx_{t-K+1} = sum_j w_j dp_{t-j}. The walk goes K - 1 tokens past the run
 // (dp there is formed again by the next run). dw and dbias: registers, then the block's shared memory,
@@ -17,7 +20,8 @@ namespace falcon {
 namespace {
 
 constexpr int kConvThreads = 256;
-constexpr int kConvBatch = 4;     // tokens whose loads are in flight together
+constexpr int kConvBatch = 4;     // tokens of a batch
+constexpr int kStages = 3;        // batches of the ring
 
 // Threads of a block: bx over the packs of one token's channels, by over runs of tokens.
 struct ConvShape {
@@ -28,7 +32,7 @@ struct ConvShape {
     long long ntb;   // blocks along the tokens
 };
 
-ConvShape conv_shape(const falcon_conv_args_t &a, int V, int run, int first) {
+ConvShape conv_shape(const falcon_conv_args_t &a, int V, int run) {
     ConvShape s;
     s.nv = (a.d + V - 1) / V;
     const long long packs = (long long)a.H * s.nv;
@@ -37,8 +41,7 @@ ConvShape conv_shape(const falcon_conv_args_t &a, int V, int run, int first) {
     s.by = kConvThreads / s.bx;
     s.run = run;
     s.ncb = (packs + s.bx - 1) / s.bx;
-    const long long tokens = (long long)a.T + first;
-    s.ntb = (tokens + (long long)run * s.by - 1) / ((long long)run * s.by);
+    s.ntb = ((long long)a.T + (long long)run * s.by - 1) / ((long long)run * s.by);
     if (s.ntb < 1) s.ntb = 1;
     return s;
 }
@@ -46,6 +49,28 @@ ConvShape conv_shape(const falcon_conv_args_t &a, int V, int run, int first) {
 template <int K> struct Taps {
     static constexpr int kPast = K > 1 ? K - 1 : 1;   // rows kept of the past (one unused row for K = 1)
 };
+
+// A thread's V channels as pairs (the upper half of the only pair is unused for V = 1).
+template <int V> struct Pairs {
+    static constexpr int N = V > 1 ? V / 2 : 1;
+};
+template <typename IO, int V>
+__device__ __forceinline__ void to_pairs(typename Pack<IO, V>::raw r, f32x2 (&o)[Pairs<V>::N]) {
+    float x[V];
+    Pack<IO, V>::cvt(r, x);
+#pragma unroll
+    for (int i = 0; i < Pairs<V>::N; ++i) o[i] = pack2(x[2 * i], x[V > 1 ? 2 * i + 1 : 0]);
+}
+template <int V>
+__device__ __forceinline__ void from_pairs(const f32x2 (&p)[Pairs<V>::N], float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < Pairs<V>::N; ++i) {
+        float lo, hi;
+        unpack2(p[i], lo, hi);
+        x[2 * i] = lo;
+        if (V > 1) x[V > 1 ? 2 * i + 1 : 0] = hi;
+    }
+}
 
 // Row r of the cached tail of (b, h): (B,H,K-1,d).
 template <typename IO, int K>
@@ -55,19 +80,53 @@ __device__ __forceinline__ IO *tail_row(const void *p, int b, int h, int H, int 
 
 template <int K, int V>
 __device__ __forceinline__ void load_weights(const falcon_conv_args_t &a, int h, int c0, float (&w)[K][V], float (&bias)[V]) {
+    const float *p = a.w + ((long long)h * a.d + c0) * K;
+    float f[K * V];   // (V channels, K taps) as they lie
+    if (V > 1 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {   // V K floats from c0 K: whole 16-byte words
+#pragma unroll
+        for (int i = 0; i + 3 < K * V; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(p + i);
+            f[i] = x.x; f[i + 1] = x.y; f[i + 2] = x.z; f[i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < K * V; ++i) f[i] = p[i];
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const long long c = (long long)h * a.d + c0 + i;
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][i] = a.w[c * K + j];
-        bias[i] = a.bias ? a.bias[c] : 0.f;
+        for (int j = 0; j < K; ++j) w[j][i] = f[i * K + j];
+        bias[i] = a.bias ? a.bias[(long long)h * a.d + c0 + i] : 0.f;
+    }
+}
+template <int K, int V>
+__device__ __forceinline__ void load_weights(const falcon_conv_args_t &a, int h, int c0, f32x2 (&w)[K][Pairs<V>::N],
+                                             f32x2 (&bias)[Pairs<V>::N]) {
+    float f[K][V], g[V];
+    load_weights<K, V>(a, h, c0, f, g);
+#pragma unroll
+    for (int i = 0; i < Pairs<V>::N; ++i) {
+        const int i1 = V > 1 ? 2 * i + 1 : 0;
+        bias[i] = pack2(g[2 * i], g[i1]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][i] = pack2(f[j][2 * i], f[j][i1]);
     }
 }
 
+// p = bias + sum_j w_j (window), oldest input first.
+template <int K, int N>
+__device__ __forceinline__ f32x2 taps(const f32x2 (&w)[K][N], const f32x2 (&past)[Taps<K>::kPast][N], f32x2 cur, f32x2 bias, int i) {
+    f32x2 p = bias;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) p = fma2(w[j][i], past[j][i], p);
+    return fma2(w[K - 1][i], cur, p);
+}
+
 template <typename IO, int K, int V, bool SILU>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(falcon_conv_args_t a, ConvShape s) {
+__global__ void __launch_bounds__(kConvThreads, K <= 5 ? 2 : 1) conv_fwd_kernel(falcon_conv_args_t a, ConvShape s) {
     typedef Pack<IO, V> P;
-    constexpr int kPast = Taps<K>::kPast;
+    constexpr int kPast = Taps<K>::kPast, N = Pairs<V>::N;
+    __shared__ __align__(16) typename P::raw ring[V > 1 ? kStages : 1][V > 1 ? kConvBatch : 1][V > 1 ? kConvThreads : 1];
     unsigned bid = blockIdx.x;
     const unsigned cb = bid % (unsigned)s.ncb;
     bid /= (unsigned)s.ncb;
@@ -78,47 +137,71 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(falcon_conv_args
     const int h = (int)(pack / s.nv), c0 = (int)(pack % s.nv) * V;
     const int n = seq_length(a.lengths, b, a.T);
     const long long tile = (long long)tb * s.by + threadIdx.y;
-    const long long t0 = tile * s.run;
-    const long long t1 = t0 + s.run < n ? t0 + s.run : n;
+    const int t0 = (int)(tile * s.run < n ? tile * s.run : n);
+    const int t1 = t0 + s.run < n ? t0 + s.run : n;
+    const int me = threadIdx.y * s.bx + threadIdx.x;
 
-    float w[K][V], bias[V];
-    load_weights<K, V>(a, h, c0, w, bias);
     const IO *x = row_of<IO>(a.x, b, h, 0) + c0;
-    IO *y = row_of<IO>(a.y, b, h, 0) + c0;
-
-    float past[kPast][V];   // x_{t-K+1} .. x_{t-1}, oldest first
-    auto extended = [&](long long t, float (&o)[V]) {   // input t, or the cached tail, or zero
-        if (t >= 0) P::cvt(P::ld(x + t * a.x.st), o);
-        else if (a.state) P::cvt(P::ld(tail_row<IO, K>(a.state, b, h, a.H, (int)(t + K - 1), a.d) + c0), o);
-        else
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = 0.f;
+    auto extended = [&](int t) {   // input t, or the cached tail, or zero
+        if (t >= 0) return P::ld(x + t * a.x.st);
+        if (a.state) return P::ld(tail_row<IO, K>(a.state, b, h, a.H, t + K - 1, a.d) + c0);
+        return P::zero();
     };
     if (t0 < t1) {
-        if (K > 1) {
+        const IO *ahead = x + t0 * a.x.st;   // the next token to be asked for
+        int ta = t0;
+        auto ask = [&](int stage) {
+            if (V > 1) {
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) extended(t0 - (K - 1) + j, past[j]);
-        }
-        for (long long t = t0; t < t1; t += kConvBatch) {
+                for (int u = 0; u < kConvBatch; ++u) {
+                    if (ta + u < t1) copy_async<sizeof(typename P::raw) == 8 ? 8 : 16>(&ring[stage][u][me], ahead);
+                    ahead += a.x.st;
+                }
+                ta += kConvBatch;
+                copy_commit();
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) ask(i);
+        f32x2 w[K][N], bias[N], past[kPast][N];   // past: x_{t-K+1} .. x_{t-1}
+        load_weights<K, V>(a, h, c0, w, bias);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) to_pairs<IO, V>(extended(t0 - (K - 1) + j), past[j]);
+        IO *y = row_of<IO>(a.y, b, h, t0) + c0;
+        int stage = 0, free_stage = kStages - 1;
+        for (int t = t0; t < t1; t += kConvBatch) {
             typename P::raw in[kConvBatch];
+            if (V > 1) {
+                ask(free_stage);
+                free_stage = free_stage + 1 < kStages ? free_stage + 1 : 0;
+                copy_wait<kStages - 1>();
 #pragma unroll
-            for (int u = 0; u < kConvBatch; ++u) in[u] = t + u < t1 ? P::ld(x + (t + u) * a.x.st) : P::zero();
+                for (int u = 0; u < kConvBatch; ++u) in[u] = ring[stage][u][me];
+                stage = stage + 1 < kStages ? stage + 1 : 0;
+            } else {
+#pragma unroll
+                for (int u = 0; u < kConvBatch; ++u) in[u] = t + u < t1 ? P::ld(x + (t + u) * a.x.st) : P::zero();
+            }
 #pragma unroll
             for (int u = 0; u < kConvBatch; ++u) {
-                float cur[V], out[V];
-                P::cvt(in[u], cur);
+                if (t + u >= t1) break;
+                f32x2 cur[N], p[N];
+                float out[V];
+                to_pairs<IO, V>(in[u], cur);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float p = bias[i];
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) p = fmaf(w[j][i], past[j][i], p);
-                    p = fmaf(w[K - 1][i], cur[i], p);
-                    out[i] = SILU ? silu(p) : p;
+                for (int i = 0; i < N; ++i) {
+                    p[i] = taps<K, N>(w, past, cur[i], bias[i], i);
 #pragma unroll
                     for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
                     if (K > 1) past[kPast - 1][i] = cur[i];
                 }
-                if (t + u < t1) P::st(y + (t + u) * a.y.st, out);
+                from_pairs<V>(p, out);
+                if (SILU) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) out[i] = silu(out[i]);
+                }
+                P::st(y, out);
+                y += a.y.st;
             }
         }
     }
@@ -127,7 +210,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(falcon_conv_args
     if (K > 1 && a.state_out && tile == 0) {
         for (int r = 0; r < K - 1; ++r) {
             float o[V];
-            extended((long long)n - (K - 1) + r, o);
+            P::cvt(extended(n - (K - 1) + r), o);
             P::st(tail_row<IO, K>(a.state_out, b, h, a.H, r, a.d) + c0, o);
         }
     }
@@ -162,13 +245,20 @@ __global__ void __launch_bounds__(128) conv_step_kernel(falcon_conv_args_t a, in
         P::st(tail_row<IO, K>(a.state_out, b, h, a.H, j, a.d) + c0, j + 1 < K - 1 ? past[j + 1 < Taps<K>::kPast ? j + 1 : 0] : cur);
 }
 
+struct True { static constexpr bool value = true; };
+struct False { static constexpr bool value = false; };
+
 template <typename IO, int K, int V, bool SILU>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(falcon_conv_args_t a, falcon_conv_grads_t g, ConvShape s,
-                                                                float *part) {
+__global__ void __launch_bounds__(kConvThreads, K <= 4 ? 2 : 1) conv_bwd_kernel(falcon_conv_args_t a, falcon_conv_grads_t g, ConvShape s,
+                                                                   float *part) {
     typedef Pack<IO, V> P;
     typedef Pack<float, V> F;
-    constexpr int kPast = Taps<K>::kPast;
-    extern __shared__ float sums[];   // kConvThreads x (K + 1) V
+    constexpr int kPast = Taps<K>::kPast, N = Pairs<V>::N;
+    extern __shared__ __align__(16) char smem[];   // the rings of dy and x, then the block's sums
+    typedef typename F::raw RingG[kConvBatch][kConvThreads];
+    typedef typename P::raw RingX[kConvBatch][kConvThreads];
+    RingG *ring_g = reinterpret_cast<RingG *>(smem);
+    RingX *ring_x = reinterpret_cast<RingX *>(smem + kStages * sizeof(RingG));
     unsigned bid = blockIdx.x;
     const unsigned cb = bid % (unsigned)s.ncb;
     bid /= (unsigned)s.ncb;
@@ -178,117 +268,182 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(falcon_conv_args
     const bool in = pack < (long long)a.H * s.nv;
     const int h = in ? (int)(pack / s.nv) : 0, c0 = in ? (int)(pack % s.nv) * V : 0;
     const int n = seq_length(a.lengths, b, a.T);
-    // the walk starts at the oldest cached token, -(K-1)
-    const long long t0 = -(K - 1) + ((long long)tb * s.by + threadIdx.y) * s.run;
-    const long long t1 = t0 + s.run < a.T ? t0 + s.run : a.T;
+    const long long tile = (long long)tb * s.by + threadIdx.y;
+    const int t0 = (int)(tile * s.run < a.T ? tile * s.run : a.T);
+    const int t1 = t0 + s.run < a.T ? t0 + s.run : a.T;
+    const int r0 = tile == 0 ? -(K - 1) : t0;   // inputs [r0, t1) get their gradient here
+    const int tend = t1 + K - 1;                // the walk's end
+    const int me = threadIdx.y * s.bx + threadIdx.x;
 
-    float dw[K][V], db[V];
+    f32x2 dw[K][N], db[N];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < N; ++i) {
+        db[i] = 0ull;
 #pragma unroll
-        for (int j = 0; j < K; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < K; ++j) dw[j][i] = 0ull;
     }
-    if (in && t0 < t1) {
-        float w[K][V], bias[V];
-        load_weights<K, V>(a, h, c0, w, bias);
+    if (in && (t0 < t1 || tile == 0)) {
         const IO *x = row_of<IO>(a.x, b, h, 0) + c0;
         const float *dy = row_of<float>(g.dy, b, h, 0) + c0;
-        float *dx = row_of<float>(g.dx, b, h, 0) + c0;
-        float past[kPast][V], dp[K][V];   // inputs before t; dp_{t-K+1} .. dp_t
-        auto extended = [&](long long t) {
+        auto extended = [&](int t) {
             if (t >= 0) return t < n ? P::ld(x + t * a.x.st) : P::zero();
-            if (t >= -(K - 1) && a.state) return P::ld(tail_row<IO, K>(a.state, b, h, a.H, (int)(t + K - 1), a.d) + c0);
+            if (t >= -(K - 1) && a.state) return P::ld(tail_row<IO, K>(a.state, b, h, a.H, t + K - 1, a.d) + c0);
             return P::zero();
         };
+        const int te = tend < n ? tend : n;     // tokens that are there
+        const IO *ahead_x = x + t0 * a.x.st;
+        const float *ahead_g = dy + t0 * g.dy.st;
+        int ta = t0;
+        auto ask = [&](int stage) {
+            if (V > 1) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+                for (int u = 0; u < kConvBatch; ++u) {
+                    if (ta + u < te) {
+                        copy_async<sizeof(typename P::raw) == 8 ? 8 : 16>(&ring_x[stage][u][me], ahead_x);
+                        copy_async<16>(&ring_g[stage][u][me], ahead_g);
+                    }
+                    ahead_x += a.x.st;
+                    ahead_g += g.dy.st;
+                }
+                ta += kConvBatch;
+                copy_commit();
+            }
+        };
 #pragma unroll
-            for (int j = 0; j < K; ++j) dp[j][i] = 0.f;
-        }
+        for (int i = 0; i < kStages - 1; ++i) ask(i);
+        f32x2 w[K][N], bias[N], past[kPast][N], dp[K][N];   // inputs before t; dp_{t-K+1} .. dp_t
+        load_weights<K, V>(a, h, c0, w, bias);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) P::cvt(extended(t0 - (K - 1) + j), past[j]);
-        for (long long tt = t0; tt < t1 + K - 1; tt += kConvBatch) {
-            typename P::raw xin[kConvBatch];
-            typename F::raw gin[kConvBatch];
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int u = 0; u < kConvBatch; ++u) {
-                const long long t = tt + u;
-                const bool live = t >= 0 && t < n && t < t1 + K - 1;
-                xin[u] = t < t1 + K - 1 ? extended(t) : P::zero();
-                gin[u] = live ? F::ld(dy + t * g.dy.st) : F::zero();
+            for (int j = 0; j < K; ++j) dp[j][i] = 0ull;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) to_pairs<IO, V>(extended(t0 - (K - 1) + j), past[j]);
+        float *dx = row_of<float>(g.dx, b, h, 0) + c0 + (t0 - (K - 1)) * g.dx.st;   // the row that the walk emits next
+
+        // One token. WHOLE: it is there, its dw is this run's, and an input of this run is complete.
+        auto token = [&](auto whole, int t, typename P::raw rx, typename F::raw rg) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            const bool live = WHOLE || t < n;
+            f32x2 cur[N], d2[N], out[N];
+            float d[V];
+            to_pairs<IO, V>(rx, cur);
+            F::cvt(rg, d);
+            if (SILU) {
+                f32x2 p2[N];
+                float p[V];
+#pragma unroll
+                for (int i = 0; i < N; ++i) p2[i] = taps<K, N>(w, past, cur[i], bias[i], i);
+                from_pairs<V>(p2, p);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] *= silu_grad(p[i]);
             }
 #pragma unroll
-            for (int u = 0; u < kConvBatch; ++u) {
-                const long long t = tt + u;
-                const bool own = t < t1;          // this run's dw
-                const bool live = t >= 0 && t < n;
-                float cur[V], gy[V], out[V];
-                P::cvt(xin[u], cur);
-                F::cvt(gin[u], gy);
+            for (int i = 0; i < N; ++i) {
+                d2[i] = pack2(d[2 * i], d[V > 1 ? 2 * i + 1 : 0]);
+                if (!live) d2[i] = 0ull;          // also where p or act'(p) is not finite
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
+                for (int j = 0; j + 1 < K; ++j) dp[j][i] = dp[j + 1][i];
+                dp[K - 1][i] = d2[i];
+                if (WHOLE || (live && t < t1)) {
 #pragma unroll
-                    for (int j = 0; j + 1 < K; ++j) dp[j][i] = dp[j + 1][i];
-                    float d = gy[i];
-                    if (SILU) {
-                        float p = bias[i];
-#pragma unroll
-                        for (int j = 0; j < K - 1; ++j) p = fmaf(w[j][i], past[j][i], p);
-                        p = fmaf(w[K - 1][i], cur[i], p);
-                        d *= silu_grad(p);
-                    }
-                    d = live ? d : 0.f;           // also where p or act'(p) is not finite
-                    dp[K - 1][i] = d;
-                    if (own && live) {
-#pragma unroll
-                        for (int j = 0; j < K - 1; ++j) dw[j][i] = fmaf(d, past[j][i], dw[j][i]);
-                        dw[K - 1][i] = fmaf(d, cur[i], dw[K - 1][i]);
-                        db[i] += d;
-                    }
-                    float o = 0.f;
-#pragma unroll
-                    for (int j = 0; j < K; ++j) o = fmaf(w[j][i], dp[K - 1 - j][i], o);
-                    out[i] = o;
-#pragma unroll
-                    for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
-                    if (K > 1) past[kPast - 1][i] = cur[i];
+                    for (int j = 0; j < K - 1; ++j) dw[j][i] = fma2(d2[i], past[j][i], dw[j][i]);
+                    dw[K - 1][i] = fma2(d2[i], cur[i], dw[K - 1][i]);
+                    db[i] = add2(db[i], d2[i]);
                 }
-                const long long r = t - (K - 1);   // the input whose gradient is complete
-                if (r < t0 || r >= t1) continue;
-                // the tail that state_out copied: extended rows n .. n + K - 2, inputs n - K + 1 .. n - 1
-                const long long tail = r + (K - 1) - n;
-                if (g.dstate_out && tail >= 0 && tail < K - 1) {
-                    const float *q = tail_row<float, K>(g.dstate_out, b, h, a.H, (int)tail, a.d) + c0;
+                out[i] = mul2(w[0][i], dp[K - 1][i]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) out[i] += q[i];
+                for (int j = 1; j < K; ++j) out[i] = fma2(w[j][i], dp[K - 1 - j][i], out[i]);
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
+                if (K > 1) past[kPast - 1][i] = cur[i];
+            }
+            float o[V];
+            from_pairs<V>(out, o);
+            if (WHOLE) {
+                F::st(dx, o);
+            } else {
+                const int r = t - (K - 1);        // the input whose gradient is complete
+                if (r >= r0 && r < t1) {
+                    // the tail that state_out copied: extended rows n .. n + K - 2, inputs n - K + 1 .. n - 1
+                    const int tail = t - n;
+                    if (g.dstate_out && tail >= 0 && tail < K - 1) {
+                        const float *q = tail_row<float, K>(g.dstate_out, b, h, a.H, tail, a.d) + c0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) o[i] += q[i];
+                    }
+                    if (r >= 0) {
+                        if (r >= n)
+#pragma unroll
+                            for (int i = 0; i < V; ++i) o[i] = 0.f;
+                        F::st(dx, o);
+                    } else if (g.dstate) {
+                        float *q = tail_row<float, K>(g.dstate, b, h, a.H, r + K - 1, a.d) + c0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) q[i] = o[i];
+                    }
                 }
-                if (r >= 0) {
-                    if (r >= n)
+            }
+            dx += g.dx.st;
+        };
+
+        const int whole0 = r0 + K - 1, whole1 = t1 < n ? t1 : n;
+        int stage = 0, free_stage = kStages - 1;
+        for (int t = t0; t < tend; t += kConvBatch) {
+            typename P::raw rx[kConvBatch];
+            typename F::raw rg[kConvBatch];
+            if (V > 1) {
+                ask(free_stage);
+                free_stage = free_stage + 1 < kStages ? free_stage + 1 : 0;
+                copy_wait<kStages - 1>();
 #pragma unroll
-                        for (int i = 0; i < V; ++i) out[i] = 0.f;
-                    F::st(dx + r * g.dx.st, out);
-                } else if (g.dstate) {
-                    float *q = tail_row<float, K>(g.dstate, b, h, a.H, (int)(r + K - 1), a.d) + c0;
+                for (int u = 0; u < kConvBatch; ++u) {
+                    rx[u] = ring_x[stage][u][me];
+                    rg[u] = ring_g[stage][u][me];
+                }
+                stage = stage + 1 < kStages ? stage + 1 : 0;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) q[i] = out[i];
+                for (int u = 0; u < kConvBatch; ++u) {
+                    rx[u] = t + u < te ? P::ld(x + (t + u) * a.x.st) : P::zero();
+                    rg[u] = t + u < te ? F::ld(dy + (t + u) * g.dy.st) : F::zero();
+                }
+            }
+            if (t >= whole0 + (tile == 0 ? K - 1 : 0) && t + kConvBatch <= whole1) {
+#pragma unroll
+                for (int u = 0; u < kConvBatch; ++u) token(True{}, t + u, rx[u], rg[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kConvBatch; ++u) {
+                    if (t + u >= tend) break;
+                    const bool there = t + u < te;   // a place of the ring that was not asked for holds anything
+                    token(False{}, t + u, there ? rx[u] : P::zero(), there ? rg[u] : F::zero());
                 }
             }
         }
+        copy_wait<0>();
     }
+    __syncthreads();   // the rings' places are free
     // the block's sums over its runs, then one partial row: (H,d,K) of dw, (H,d) of dbias
     constexpr int M = (K + 1) * V;
-    float *mine = sums + (threadIdx.y * s.bx + threadIdx.x) * M;
+    float *sums = reinterpret_cast<float *>(smem);
+    float *mine = sums + me * M;
+    {
+        float f[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int j = 0; j < K; ++j) {
+            from_pairs<V>(dw[j], f);
 #pragma unroll
-        for (int j = 0; j < K; ++j) mine[i * K + j] = dw[j][i];
-        mine[K * V + i] = db[i];
+            for (int i = 0; i < V; ++i) mine[i * K + j] = f[i];
+        }
+        from_pairs<V>(db, f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) mine[K * V + i] = f[i];
     }
     __syncthreads();
     const long long HD = (long long)a.H * a.d;
     float *row = part + ((long long)b * s.ntb + tb) * HD * (K + 1);
-    for (int e = threadIdx.y * s.bx + threadIdx.x; e < s.bx * M; e += kConvThreads) {
+    for (int e = me; e < s.bx * M; e += kConvThreads) {
         float acc = 0.f;
         for (int y = 0; y < s.by; ++y) acc += sums[(long long)y * s.bx * M + e];
         const long long pk = (long long)cb * s.bx + e / M;
@@ -296,7 +451,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(falcon_conv_args
         const int m = e % M;
         const long long c = pk / s.nv * a.d + pk % s.nv * V;
         if (m < K * V) row[c * K + m] = acc;
-        else row[(long long)HD * K + c + (m - K * V)] = acc;
+        else row[HD * K + c + (m - K * V)] = acc;
     }
 }
 
@@ -315,7 +470,7 @@ int conv_pack(const falcon_conv_args_t &a, const falcon_view_t *f32a, const falc
 // Tokens of a thread's run: long runs re-read less of the past, short ones give more threads.
 int conv_run(const falcon_conv_args_t &a, int V, long long want_threads) {
     const long long packs = (long long)a.H * ((a.d + V - 1) / V) * a.B;
-    int run = 64;
+    int run = 128;
     while (run > 8 && packs * ((a.T + run - 1) / run) < want_threads) run /= 2;
     return run;
 }
@@ -364,17 +519,23 @@ cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &
     const long long blocks = s.ncb * s.ntb * a.B;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const dim3 block(s.bx, s.by);
-    const size_t smem = (size_t)kConvThreads * (a.K + 1) * V * sizeof(float);
+    const size_t ring = V > 1 ? (size_t)kStages * kConvBatch * kConvThreads * V * (sizeof(float) + sizeof(IO)) : 0;
+    const size_t sums = (size_t)kConvThreads * (a.K + 1) * V * sizeof(float);
+    const size_t smem = ring > sums ? ring : sums;
 #define FALCON_RUN(K)                                                                             \
-    if (a.act == FALCON_ACT_SILU) conv_bwd_kernel<IO, K, V, true><<<(unsigned)blocks, block, smem, st>>>(a, g, s, ws); \
-    else conv_bwd_kernel<IO, K, V, false><<<(unsigned)blocks, block, smem, st>>>(a, g, s, ws)
+    {                                                                                             \
+        const auto kern = a.act == FALCON_ACT_SILU ? conv_bwd_kernel<IO, K, V, true> : conv_bwd_kernel<IO, K, V, false>; \
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
+        if (e != cudaSuccess) return e;                                                           \
+        kern<<<(unsigned)blocks, block, smem, st>>>(a, g, s, ws);                                 \
+    }
     FALCON_CONV_TAPS(FALCON_RUN)
 #undef FALCON_RUN
     return cudaGetLastError();
 }
 
 ConvShape conv_bwd_shape(const falcon_conv_args_t &a, int V) {
-    return conv_shape(a, V, conv_run(a, V, 148 * 1024), a.K - 1);
+    return conv_shape(a, V, conv_run(a, V, 148 * 1024));
 }
 
 }  // namespace
@@ -382,7 +543,7 @@ ConvShape conv_bwd_shape(const falcon_conv_args_t &a, int V) {
 cudaError_t launch_conv_fwd(const falcon_conv_args_t &a, int num_sms, cudaStream_t st) {
     if ((long long)a.B * a.H == 0) return cudaSuccess;
     const int V = conv_pack(a, nullptr, nullptr);
-    const ConvShape s = conv_shape(a, V, conv_run(a, V, (long long)num_sms * 2048), 0);
+    const ConvShape s = conv_shape(a, V, conv_run(a, V, (long long)num_sms * 2048));
     if (a.io_dtype == FALCON_BF16)
         return V == 8 ? conv_fwd_io<__nv_bfloat16, 8>(a, s, st) : conv_fwd_io<__nv_bfloat16, 1>(a, s, st);
     return V == 4 ? conv_fwd_io<float, 4>(a, s, st) : conv_fwd_io<float, 1>(a, s, st);

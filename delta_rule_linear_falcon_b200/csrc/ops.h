@@ -40,8 +40,7 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
 
 // norm of queries and keys (qknorm.cu)
 size_t qknorm_bwd_workspace(const falcon_qknorm_args_t &a);
-cudaError_t launch_qknorm_fwd(const falcon_qknorm_args_t &a, int num_sms, cudaStream_t s);
-cudaError_t launch_qknorm_bwd(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t &g, float *ws,
-                              int num_sms, cudaStream_t s);
+cudaError_t launch_qknorm_fwd(const falcon_qknorm_args_t &a, cudaStream_t s);
+cudaError_t launch_qknorm_bwd(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t &g, float *ws, cudaStream_t s);
 
 }  // namespace falcon
