@@ -17,6 +17,13 @@ template <> struct Pack<float, 1> {
     static __device__ __forceinline__ void cvt(raw r, float (&x)[1]) { x[0] = r; }
     static __device__ __forceinline__ void st(float *p, const float (&x)[1]) { *p = x[0]; }
 };
+template <> struct Pack<float, 2> {
+    typedef float2 raw;
+    static __device__ __forceinline__ raw ld(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+    static __device__ __forceinline__ raw zero() { return make_float2(0.f, 0.f); }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[2]) { x[0] = r.x; x[1] = r.y; }
+    static __device__ __forceinline__ void st(float *p, const float (&x)[2]) { *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]); }
+};
 template <> struct Pack<float, 4> {
     typedef float4 raw;
     static __device__ __forceinline__ raw ld(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -24,23 +31,6 @@ template <> struct Pack<float, 4> {
     static __device__ __forceinline__ void cvt(raw r, float (&x)[4]) { x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w; }
     static __device__ __forceinline__ void st(float *p, const float (&x)[4]) {
         *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    }
-};
-template <> struct Pack<float, 8> {
-    struct raw { float4 a, b; };
-    static __device__ __forceinline__ raw ld(const float *p) {
-        return raw{reinterpret_cast<const float4 *>(p)[0], reinterpret_cast<const float4 *>(p)[1]};
-    }
-    static __device__ __forceinline__ raw zero() {
-        return raw{make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    }
-    static __device__ __forceinline__ void cvt(raw r, float (&x)[8]) {
-        x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-        x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-    }
-    static __device__ __forceinline__ void st(float *p, const float (&x)[8]) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 template <> struct Pack<__nv_bfloat16, 1> {

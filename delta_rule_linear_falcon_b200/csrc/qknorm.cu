@@ -2,13 +2,15 @@
 // the rotation by position in the same pass.
 //
 // A row is read once and written once for a few flops an element: bound by HBM. A row of d channels
-// belongs to LANES neighbouring lanes with NV packs of 16 bytes each (of the io type), so a warp moves
-// whole rows; the sum of squares and the partner of a rotated pair come from shuffles (the partner of
-// FALCON_ROT_HALF is rot / 2 channels away, a whole number of packs). A group of LANES lanes takes one token
-// and walks its heads, kRows of them in flight: the token's sines and cosines, the same for every head, are
-// formed once by the block (the angle's whole turns taken off in fp64), kept in registers over the walk, and
-// the row addresses advance by one addition. With few tokens the heads are cut over more groups.
-// Where pointers, strides, d or rot / 2 are not multiples of a pack, V = 1: lane l owns channels l, l + 32, ..
+// belongs to LANES neighbouring lanes with NV packs of V channels each (16 bytes of the io type), so a warp
+// moves whole rows; the sum of squares comes from shuffles. Both channels of a rotated pair are in one lane: a
+// pack of FALCON_ROT_HALF is V / 2 channels of the lower half and the V / 2 that turn with them (two 8-byte
+// accesses; exchanging packs between lanes took a shuffle for every channel: 98 us instead of 88 for 134M
+// channels in bf16). A group of LANES lanes takes one token and walks its heads, kRows of them in flight: the
+// token's sines and cosines, the same for every head, are formed once by the block (the angle's whole turns
+// taken off in fp64), kept in registers over the walk, and the row addresses advance by one addition. With few
+// tokens the heads are cut over more groups.
+// Where pointers, strides, d or rot are not multiples of a pack, V = 1: lane l owns channels l, l + 32, ..
 // and partners come through shared memory.
 // Backward: the same walk with the row turned back; dwq and dwk are summed per lane over the tokens of a
 // block, then over blocks by a second launch.
@@ -29,20 +31,18 @@ struct NormShape {
     int parts;          // walks of a token
 };
 
-// Where pair p's (cos, sin) lies: V > 1 as 16-byte pairs of pairs, [pair of the pack][pack], so that the lanes
-// of a row read neighbouring words.
+// Where pair p's (cos, sin) lies. V > 1: V / 2 pairs a pack, two of them in 16 bytes, [two pairs of the
+// pack][pack], so that the lanes of a row read neighbouring words.
 template <int V>
 __device__ __forceinline__ int turn_slot(const falcon_qknorm_args_t &a, int p) {
     if (V == 1) return p;
-    const int per = a.rot_layout == FALCON_ROT_HALF ? V : V / 2;   // pairs of a pack
-    const int packs = (a.rot / 2 + per - 1) / per;
-    return ((p % per) / 2 * packs + p / per) * 2 + (p & 1);
+    constexpr int H = V > 1 ? V / 2 : 1;
+    const int packs = (a.rot + V - 1) / V;
+    return ((p % H) / 2 * packs + p / H) * 2 + (p & 1);
 }
 // Slots of a token (the last pack may be padded).
 __host__ __device__ inline int turn_slots(const falcon_qknorm_args_t &a, int V) {
-    if (V == 1) return a.rot / 2;
-    const int per = a.rot_layout == FALCON_ROT_HALF ? V : V / 2;
-    return (a.rot / 2 + per - 1) / per * per;
+    return V == 1 ? a.rot / 2 : (a.rot + V - 1) / V * (V / 2);
 }
 
 // Sines and cosines of `tokens` tokens from tok0 on. Padded pairs turn by nothing.
@@ -63,10 +63,10 @@ __device__ __forceinline__ void angles(const falcon_qknorm_args_t &a, long long 
     }
 }
 
-// 1 / root of a row with sum of squares ss.
-__device__ __forceinline__ float root_inverse(const falcon_qknorm_args_t &a, float ss) {
+// 1 / root of a row with sum of squares ss; scale is 1 / d for FALCON_NORM_RMS, else 1.
+__device__ __forceinline__ float root_inverse(const falcon_qknorm_args_t &a, float ss, float scale) {
     if (a.norm == FALCON_NORM_NONE) return 1.f;
-    const float m = (a.norm == FALCON_NORM_RMS ? ss / (float)a.d : ss) + a.eps;
+    const float m = fmaf(ss, scale, a.eps);
     return m == 0.f ? 0.f : rsqrtf(m);
 }
 
@@ -77,103 +77,137 @@ __device__ __forceinline__ float lanes_total(float x) {
     return x;
 }
 
-// A lane's part of a token's rotation: for each of its packs' channels the factors of the channel itself (c) and of
-// its partner (s, with the partner's sign).
-template <int V, int LANES, int NV, bool HALF> struct Turn {
-    float c[NV][V], s[NV][V];
-    int froms[NV];   // HALF: the pack of each pack's partners (V = 1: the partner's channel)
+// Backward: rows in flight in the ring (few enough for two blocks an SM), and the bytes before it.
+__host__ __device__ constexpr int norm_ring(int V, int NV) { return V == 1 ? 1 : NV > 1 ? 3 : 5; }
+__host__ __device__ inline size_t norm_turn_bytes(const falcon_qknorm_args_t &a, int V, int tokens) {
+    return ((size_t)tokens * turn_slots(a, V) * sizeof(float2) + 15) / 16 * 16;
+}
 
+// A pack of a row in registers: the first channels of its pairs, then the second ones. `row` points at the row's
+// first channel.
+template <typename E, int V, bool HALF> struct Row {
+    static constexpr int H = V / 2;
+    typedef Pack<E, H> P;
+    struct raw { typename P::raw a, b; };
+    static __device__ __forceinline__ int first(int p, int rot) { return HALF && p * V < rot ? p * H : p * V; }
+    static __device__ __forceinline__ int second(int p, int rot) { return HALF && p * V < rot ? rot / 2 + p * H : p * V + H; }
+    static __device__ __forceinline__ int channel(int p, int i, int rot) {
+        if (!HALF) return p * V + (i < H ? 2 * i : 2 * (i - H) + 1);
+        return i < H ? first(p, rot) + i : second(p, rot) + i - H;
+    }
+    // where a pack's halves lie, formed once for all rows
+    struct Place {
+        int a, b;
+        __device__ __forceinline__ Place(int p, int rot) : a(first(p, rot)), b(second(p, rot)) {}
+    };
+    static __device__ __forceinline__ raw zero() { return raw{P::zero(), P::zero()}; }
+    static __device__ __forceinline__ raw ld(const E *row, Place at) { return raw{P::ld(row + at.a), P::ld(row + at.b)}; }
+    static __device__ __forceinline__ void ask(raw *to, const E *row, Place at) {
+        copy_async<sizeof(typename P::raw)>(&to->a, row + at.a);
+        copy_async<sizeof(typename P::raw)>(&to->b, row + at.b);
+    }
+    static __device__ __forceinline__ void cvt(const raw &r, float (&x)[V]) {
+        float u[H], v[H];
+        P::cvt(r.a, u);
+        P::cvt(r.b, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float y = HALF ? (i < H ? u[i % H] : v[i % H]) : (channel(0, i, 0) < H ? u[channel(0, i, 0) % H] : v[channel(0, i, 0) % H]);
+            x[i] = y;
+        }
+    }
+    static __device__ __forceinline__ void st(E *row, Place at, const float (&x)[V]) {
+        float u[H], v[H];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int j = HALF ? i : channel(0, i, 0);
+            if (j < H) u[j % H] = x[i];
+            else v[j % H] = x[i];
+        }
+        P::st(row + at.a, u);
+        P::st(row + at.b, v);
+    }
+};
+template <typename E, bool HALF> struct Row<E, 1, HALF> {
+    typedef Pack<E, 1> P;
+    typedef typename P::raw raw;
+    struct Place {
+        int a;
+        __device__ __forceinline__ Place(int p, int) : a(p) {}
+    };
+    static __device__ __forceinline__ int channel(int p, int, int) { return p; }
+    static __device__ __forceinline__ raw zero() { return P::zero(); }
+    static __device__ __forceinline__ raw ld(const E *row, Place at) { return P::ld(row + at.a); }
+    static __device__ __forceinline__ void ask(raw *, const E *, Place) {}
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[1]) { P::cvt(r, x); }
+    static __device__ __forceinline__ void st(E *row, Place at, const float (&x)[1]) { P::st(row + at.a, x); }
+};
+
+// A lane's part of a token's rotation: the factors of its pairs.
+template <int V, int LANES, int NV, bool HALF> struct Turn {
+    static constexpr int H = V / 2;
+    float c[NV][H], s[NV][H];
+    __device__ __forceinline__ void load(const falcon_qknorm_args_t &a, int lane, const float2 *cs, float sign) {
+        const int packs = (a.rot + V - 1) / V;
+#pragma unroll
+        for (int m = 0; m < NV; ++m) {
+            const int p = lane + m * LANES;
+#pragma unroll
+            for (int i = 0; i < H; i += 2) {
+                float4 r = make_float4(1.f, 0.f, 1.f, 0.f);
+                if (p < packs) r = reinterpret_cast<const float4 *>(cs)[i / 2 * packs + p];
+                c[m][i] = r.x;
+                s[m][i] = sign * r.y;
+                c[m][i + 1 < H ? i + 1 : i] = r.z;
+                s[m][i + 1 < H ? i + 1 : i] = sign * r.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void apply(float (&n)[NV][V], int, float *) const {
+#pragma unroll
+        for (int m = 0; m < NV; ++m)
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float x1 = n[m][i], x2 = n[m][H + i];
+                n[m][i] = fmaf(x1, c[m][i], -x2 * s[m][i]);
+                n[m][H + i] = fmaf(x2, c[m][i], x1 * s[m][i]);
+            }
+    }
+};
+// One channel a pack: the factor of the channel itself, its partner, and the partner's factor with its sign.
+template <int LANES, int NV, bool HALF> struct Turn<1, LANES, NV, HALF> {
+    float c[NV], s[NV];
+    int from[NV];
     __device__ __forceinline__ void load(const falcon_qknorm_args_t &a, int lane, const float2 *cs, float sign) {
         const int half = a.rot / 2;
 #pragma unroll
         for (int m = 0; m < NV; ++m) {
             const int p = lane + m * LANES;
-            froms[m] = p;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                c[m][i] = 1.f;
-                s[m][i] = 0.f;
-            }
-            if (V == 1) {
-                if (p < a.rot) {
-                    const bool hi = HALF ? p >= half : (p & 1) != 0;
-                    froms[m] = HALF ? (hi ? p - half : p + half) : p ^ 1;
-                    const float2 r = cs[HALF ? (hi ? p - half : p) : p / 2];
-                    c[m][0] = r.x;
-                    s[m][0] = (hi ? sign : -sign) * r.y;
-                }
-            } else if (HALF) {
-                const int hp = half / V;
-                if (p < 2 * hp) {
-                    const bool hi = p >= hp;
-                    froms[m] = hi ? p - hp : p + hp;
-                    const float f = hi ? sign : -sign;
-#pragma unroll
-                    for (int i = 0; i < V; i += 2) {
-                        const float4 r = reinterpret_cast<const float4 *>(cs)[i / 2 * hp + (hi ? p - hp : p)];
-                        c[m][i] = r.x;
-                        s[m][i] = f * r.y;
-                        c[m][i + 1 < V ? i + 1 : i] = r.z;
-                        s[m][i + 1 < V ? i + 1 : i] = f * r.w;
-                    }
-                }
-            } else {
-                const int packs = (half + V / 2 - 1) / (V > 1 ? V / 2 : 1);
-                if (p < packs) {
-#pragma unroll
-                    for (int i = 0; i + 3 < V; i += 4) {
-                        const float4 r = reinterpret_cast<const float4 *>(cs)[i / 4 * packs + p];
-                        c[m][i] = c[m][i + 1] = r.x;
-                        s[m][i] = -sign * r.y;
-                        s[m][i + 1] = sign * r.y;
-                        c[m][i + 2] = c[m][i + 3] = r.z;
-                        s[m][i + 2] = -sign * r.w;
-                        s[m][i + 3] = sign * r.w;
-                    }
-                }
+            c[m] = 1.f;
+            s[m] = 0.f;
+            from[m] = p;
+            if (p < a.rot) {
+                const bool hi = HALF ? p >= half : (p & 1) != 0;
+                from[m] = HALF ? (hi ? p - half : p + half) : p ^ 1;
+                const float2 r = cs[HALF ? (hi ? p - half : p) : p / 2];
+                c[m] = r.x;
+                s[m] = (hi ? sign : -sign) * r.y;
             }
         }
     }
-
-    // n <- the row turned; stage: the warp's shared row (V = 1).
-    __device__ __forceinline__ void apply(float (&n)[NV][V], int lane, float *stage) const {
-        float o[NV][V];
-        if (V == 1) {
-            __syncwarp();
+    __device__ __forceinline__ void apply(float (&n)[NV][1], int lane, float *stage) const {   // stage: the warp's row
+        __syncwarp();
 #pragma unroll
-            for (int m = 0; m < NV; ++m) stage[lane + m * LANES] = n[m][0];
-            __syncwarp();
+        for (int m = 0; m < NV; ++m) stage[lane + m * LANES] = n[m][0];
+        __syncwarp();
 #pragma unroll
-            for (int m = 0; m < NV; ++m) o[m][0] = stage[froms[m]];
-        } else if (HALF) {
-#pragma unroll
-            for (int m = 0; m < NV; ++m)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float x = 0.f;
-#pragma unroll
-                    for (int mm = 0; mm < NV; ++mm) {
-                        const float y = __shfl_sync(0xffffffffu, n[mm][i], froms[m] % LANES, LANES);
-                        if (NV == 1 || froms[m] / LANES == mm) x = y;
-                    }
-                    o[m][i] = x;
-                }
-        } else {
-#pragma unroll
-            for (int m = 0; m < NV; ++m)
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[m][i] = n[m][V > 1 ? i ^ 1 : i];
-        }
-#pragma unroll
-        for (int m = 0; m < NV; ++m)
-#pragma unroll
-            for (int i = 0; i < V; ++i) n[m][i] = fmaf(n[m][i], c[m][i], o[m][i] * s[m][i]);
+        for (int m = 0; m < NV; ++m) n[m][0] = fmaf(n[m][0], c[m], stage[from[m]] * s[m]);
     }
 };
 
 template <typename IO, int V, int LANES, int NV, bool HALF>
 __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_args_t a, NormShape s) {
-    typedef Pack<IO, V> P;
+    typedef Row<IO, V, HALF> R;
     constexpr int G = kNormThreads / LANES;       // groups of lanes, tokens of a block
     constexpr int kRows = V == 1 ? 1 : 4 / NV;    // rows in flight
     extern __shared__ __align__(16) float2 cs[];
@@ -192,6 +226,7 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_
     const int b = live ? (int)(tok / a.T) : 0, t = live ? (int)(tok - (long long)b * a.T) : 0;
     live = live && t < seq_length(a.lengths, b, a.T);
     const int h0 = blockIdx.y * s.heads, h1 = min(h0 + s.heads, a.Hq + a.Hk);
+    const float scale = a.norm == FALCON_NORM_RMS ? 1.f / (float)a.d : 1.f;
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {      // queries, then keys
         const falcon_view_t &in = which ? a.k : a.q, &out = which ? a.k_out : a.q_out;
@@ -203,40 +238,81 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_
         for (int m = 0; m < NV; ++m)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = (lane + m * LANES) * V + i;
-                w[m][i] = weight && e < a.d ? weight[e] : 1.f;
+                const int p = lane + m * LANES;
+                w[m][i] = weight && p * V < a.d ? weight[R::channel(p, i, a.rot)] : 1.f;
             }
-        const IO *px = row_of<IO>(in, b, first, t) + lane * V;
-        IO *po = row_of<IO>(out, b, first, t) + lane * V;
+        // the weights go into the rotation: a pair (x1, x2) becomes (x1 c1 - x2 s2, x2 c2 + x1 s1) / root
+        constexpr int Q = V > 1 ? V / 4 : 1;
+        f32x2 c1[NV][Q], s1[NV][Q], c2[NV][Q], s2[NV][Q];
+        if constexpr (V > 1) {
+#pragma unroll
+            for (int m = 0; m < NV; ++m)
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    constexpr int H = V / 2;
+                    const int j = 2 * i;
+                    const float ca = a.rot > 0 ? turn.c[m][j] : 1.f, cb = a.rot > 0 ? turn.c[m][j + 1] : 1.f;
+                    const float sa = a.rot > 0 ? turn.s[m][j] : 0.f, sb = a.rot > 0 ? turn.s[m][j + 1] : 0.f;
+                    c1[m][i] = pack2(w[m][j] * ca, w[m][j + 1] * cb);
+                    s1[m][i] = pack2(w[m][j] * sa, w[m][j + 1] * sb);
+                    c2[m][i] = pack2(w[m][H + j] * ca, w[m][H + j + 1] * cb);
+                    s2[m][i] = pack2(-w[m][H + j] * sa, -w[m][H + j + 1] * sb);
+                }
+        }
+        const IO *px = row_of<IO>(in, b, first, t);
+        IO *po = row_of<IO>(out, b, first, t);
         for (int h = first; h < last; h += kRows) {
-            typename P::raw raw[kRows][NV];
+            typename R::raw raw[kRows][NV];
 #pragma unroll
             for (int r = 0; r < kRows; ++r)
 #pragma unroll
                 for (int m = 0; m < NV; ++m) {
-                    raw[r][m] = P::zero();
-                    if (live && h + r < last && (lane + m * LANES) * V < a.d) raw[r][m] = P::ld(px + r * in.sh + m * LANES * V);
+                    raw[r][m] = R::zero();
+                    if (live && h + r < last && (lane + m * LANES) * V < a.d)
+                        raw[r][m] = R::ld(px + r * in.sh, typename R::Place(lane + m * LANES, a.rot));
                 }
             px += kRows * in.sh;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                float x[NV][V], ss = 0.f;
+                float x[NV][V];
 #pragma unroll
-                for (int m = 0; m < NV; ++m) {
-                    P::cvt(raw[r][m], x[m]);
+                for (int m = 0; m < NV; ++m) R::cvt(raw[r][m], x[m]);
+                if constexpr (V > 1) {
+                    constexpr int H = V / 2;
+                    f32x2 x1[NV][Q], x2[NV][Q], sq = 0ull;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) ss = fmaf(x[m][i], x[m][i], ss);
+                    for (int m = 0; m < NV; ++m)
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            x1[m][i] = pack2(x[m][2 * i], x[m][2 * i + 1]);
+                            x2[m][i] = pack2(x[m][H + 2 * i], x[m][H + 2 * i + 1]);
+                            sq = fma2(x1[m][i], x1[m][i], sq);
+                            sq = fma2(x2[m][i], x2[m][i], sq);
+                        }
+                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(sum2(sq)), scale);
+                    const f32x2 ri2 = pack2(ri, ri);
+#pragma unroll
+                    for (int m = 0; m < NV; ++m)
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            const f32x2 y1 = mul2(ri2, fma2(x1[m][i], c1[m][i], mul2(x2[m][i], s2[m][i])));
+                            const f32x2 y2 = mul2(ri2, fma2(x2[m][i], c2[m][i], mul2(x1[m][i], s1[m][i])));
+                            unpack2(y1, x[m][2 * i], x[m][2 * i + 1]);
+                            unpack2(y2, x[m][H + 2 * i], x[m][H + 2 * i + 1]);
+                        }
+                } else {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int m = 0; m < NV; ++m) ss = fmaf(x[m][0], x[m][0], ss);
+                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss), scale);
+#pragma unroll
+                    for (int m = 0; m < NV; ++m) x[m][0] = x[m][0] * ri * w[m][0];
+                    if (a.rot > 0) turn.apply(x, lane, stage);
                 }
-                const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss));
-#pragma unroll
-                for (int m = 0; m < NV; ++m)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) x[m][i] = x[m][i] * ri * w[m][i];
-                if (a.rot > 0) turn.apply(x, lane, stage);
                 if (live && h + r < last) {
 #pragma unroll
                     for (int m = 0; m < NV; ++m)
-                        if ((lane + m * LANES) * V < a.d) P::st(po + r * out.sh + m * LANES * V, x[m]);
+                        if ((lane + m * LANES) * V < a.d) R::st(po + r * out.sh, typename R::Place(lane + m * LANES, a.rot), x[m]);
                 }
             }
             po += kRows * out.sh;
@@ -245,26 +321,67 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_
 }
 
 template <typename IO, int V, int LANES, int NV, bool HALF>
-__global__ void __launch_bounds__(kNormThreads) qknorm_bwd_kernel(falcon_qknorm_args_t a, falcon_qknorm_grads_t g, NormShape s,
+__global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kernel(falcon_qknorm_args_t a, falcon_qknorm_grads_t g, NormShape s,
                                                                   float *part) {
-    typedef Pack<IO, V> P;
-    typedef Pack<float, V> F;
+    typedef Row<IO, V, HALF> R;
+    typedef Row<float, V, HALF> F;
     constexpr int G = kNormThreads / LANES;
-    constexpr int kRows = V == 1 || NV > 1 ? 1 : 2;
-    extern __shared__ __align__(16) float2 cs[];
+    constexpr int RING = norm_ring(V, NV);          // rows in flight
+    extern __shared__ __align__(16) char smem[];    // the rotation's factors, then the ring
+    float2 *cs = reinterpret_cast<float2 *>(smem);
+    typedef typename R::raw RingX[NV][kNormThreads];
+    typedef typename F::raw RingU[NV][kNormThreads];
+    RingU *ring_u = reinterpret_cast<RingU *>(smem + norm_turn_bytes(a, V, G));
+    RingX *ring_x = reinterpret_cast<RingX *>(ring_u + RING);
     __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
     __shared__ float sw[2][kMaxWidth];
     float *stage = stage_all[V == 1 ? threadIdx.x >> 5 : 0];
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const long long walks = s.groups * s.parts;
-    float dw[2][NV][V];
+    const float scale = a.norm == FALCON_NORM_RMS ? 1.f / (float)a.d : 1.f;
+    constexpr int NP = V > 1 ? V / 2 : 1;
+    f32x2 dw2[2][NV][NP];   // V > 1: the first channels of the pairs, then the second
+    float dw[2][NV];        // V = 1
 #pragma unroll
-    for (int m = 0; m < NV; ++m)
+    for (int m = 0; m < NV; ++m) {
+        dw[0][m] = dw[1][m] = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[0][m][i] = dw[1][m][i] = 0.f;
+        for (int i = 0; i < NP; ++i) dw2[0][m][i] = dw2[1][m][i] = 0ull;
+    }
     for (long long walk = blockIdx.x; walk < walks; walk += gridDim.x) {
         const long long tok0 = walk / s.parts * G;
         const int h0 = (int)(walk % s.parts) * s.heads, h1 = min(h0 + s.heads, a.Hq + a.Hk);
+        const long long tok = tok0 + slot;
+        const bool there = tok < (long long)a.B * a.T;
+        const int b = there ? (int)(tok / a.T) : 0, t = there ? (int)(tok - (long long)b * a.T) : 0;
+        const bool live = there && t < seq_length(a.lengths, b, a.T);
+
+        // the rows of the walk, queries and then keys, asked for ahead of their use
+        int ha = h0;
+        const IO *ahead_x = ha < a.Hq ? row_of<IO>(a.q, b, ha, t) : row_of<IO>(a.k, b, ha - a.Hq, t);
+        const float *ahead_u = ha < a.Hq ? row_of<float>(g.dq_out, b, ha, t) : row_of<float>(g.dk_out, b, ha - a.Hq, t);
+        auto ask = [&](int place) {
+            if (V == 1) return;
+            if (live && ha < h1) {
+#pragma unroll
+                for (int m = 0; m < NV; ++m)
+                    if ((lane + m * LANES) * V < a.d) {
+                        R::ask(&ring_x[place][m][threadIdx.x], ahead_x, typename R::Place(lane + m * LANES, a.rot));
+                        F::ask(&ring_u[place][m][threadIdx.x], ahead_u, typename F::Place(lane + m * LANES, a.rot));
+                    }
+            }
+            ++ha;
+            ahead_x += ha > a.Hq ? a.k.sh : a.q.sh;
+            ahead_u += ha > a.Hq ? g.dk_out.sh : g.dq_out.sh;
+            if (ha == a.Hq && a.Hk > 0) {
+                ahead_x = row_of<IO>(a.k, b, 0, t);
+                ahead_u = row_of<float>(g.dk_out, b, 0, t);
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) ask(i);
+
         Turn<V, LANES, NV, HALF> turn;
         if (a.rot > 0) {
             __syncthreads();
@@ -272,10 +389,7 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_bwd_kernel(falcon_qknorm_
             __syncthreads();
             turn.load(a, lane, cs + slot * turn_slots(a, V), -1.f);
         }
-        const long long tok = tok0 + slot;
-        const bool there = tok < (long long)a.B * a.T;
-        const int b = there ? (int)(tok / a.T) : 0, t = there ? (int)(tok - (long long)b * a.T) : 0;
-        const bool live = there && t < seq_length(a.lengths, b, a.T);
+        int place = 0, free_place = RING - 1;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const falcon_view_t &in = which ? a.k : a.q, &up = which ? g.dk_out : g.dq_out, &to = which ? g.dk : g.dq;
@@ -287,70 +401,110 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_bwd_kernel(falcon_qknorm_
             for (int m = 0; m < NV; ++m)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int e = (lane + m * LANES) * V + i;
-                    w[m][i] = weight && e < a.d ? weight[e] : 1.f;
+                    const int p = lane + m * LANES;
+                    w[m][i] = weight && p * V < a.d ? weight[R::channel(p, i, a.rot)] : 1.f;
                 }
-            const IO *px = row_of<IO>(in, b, first, t) + lane * V;
-            const float *pu = row_of<float>(up, b, first, t) + lane * V;
-            float *po = row_of<float>(to, b, first, t) + lane * V;
-            for (int h = first; h < last; h += kRows) {
-                typename P::raw rx[kRows][NV];
-                typename F::raw ru[kRows][NV];
+            float *po = row_of<float>(to, b, first, t);
+            for (int h = first; h < last; ++h) {
+                float x[NV][V], u[NV][V];
+                if (V > 1) {
+                    ask(free_place);
+                    free_place = free_place + 1 < RING ? free_place + 1 : 0;
+                    copy_wait<RING - 1>();
+                }
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
-#pragma unroll
-                    for (int m = 0; m < NV; ++m) {
-                        rx[r][m] = P::zero();
-                        ru[r][m] = F::zero();
-                        if (live && h + r < last && (lane + m * LANES) * V < a.d) {
-                            rx[r][m] = P::ld(px + r * in.sh + m * LANES * V);
-                            ru[r][m] = F::ld(pu + r * up.sh + m * LANES * V);
-                        }
+                for (int m = 0; m < NV; ++m) {
+                    const int p = lane + m * LANES;
+                    const bool mine = live && p * V < a.d;
+                    typename R::raw rx = R::zero();
+                    typename F::raw ru = F::zero();
+                    if (mine) {
+                        rx = V > 1 ? ring_x[place][m][threadIdx.x] : R::ld(row_of<IO>(in, b, h, t), typename R::Place(p, a.rot));
+                        ru = V > 1 ? ring_u[place][m][threadIdx.x] : F::ld(row_of<float>(up, b, h, t), typename F::Place(p, a.rot));
                     }
-                px += kRows * in.sh;
-                pu += kRows * up.sh;
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    float x[NV][V], u[NV][V], ss = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int m = 0; m < NV; ++m) {
-                        P::cvt(rx[r][m], x[m]);
-                        F::cvt(ru[r][m], u[m]);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) ss = fmaf(x[m][i], x[m][i], ss);
-                    }
-                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss));
-                    if (a.rot > 0) turn.apply(u, lane, stage);
+                    R::cvt(rx, x[m]);
+                    F::cvt(ru, u[m]);
+                }
+                if (V > 1) place = place + 1 < RING ? place + 1 : 0;
+                if constexpr (V > 1) {   // two channels an instruction
+                    constexpr int H = V / 2, Q = V / 4;
+                    f32x2 x1[NV][Q], x2[NV][Q], u1[NV][Q], u2[NV][Q], sum = 0ull;
 #pragma unroll
                     for (int m = 0; m < NV; ++m)
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            x[m][i] *= ri;
-                            if (live && h + r < last) dw[which][m][i] = fmaf(u[m][i], x[m][i], dw[which][m][i]);
-                            u[m][i] *= w[m][i];
-                            dot = fmaf(u[m][i], x[m][i], dot);
+                        for (int i = 0; i < Q; ++i) {
+                            x1[m][i] = pack2(x[m][2 * i], x[m][2 * i + 1]);
+                            x2[m][i] = pack2(x[m][H + 2 * i], x[m][H + 2 * i + 1]);
+                            sum = fma2(x1[m][i], x1[m][i], sum);
+                            sum = fma2(x2[m][i], x2[m][i], sum);
                         }
-                    if (a.norm != FALCON_NORM_NONE) {
-                        dot = lanes_total<LANES>(dot);
-                        if (a.norm == FALCON_NORM_RMS) dot /= (float)a.d;
+                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(sum2(sum)), scale);
+                    const f32x2 ri2 = pack2(ri, ri);
+                    sum = 0ull;
 #pragma unroll
-                        for (int m = 0; m < NV; ++m)
+                    for (int m = 0; m < NV; ++m)
 #pragma unroll
-                            for (int i = 0; i < V; ++i) u[m][i] = ri * fmaf(-x[m][i], dot, u[m][i]);
+                        for (int i = 0; i < Q; ++i) {
+                            u1[m][i] = pack2(u[m][2 * i], u[m][2 * i + 1]);
+                            u2[m][i] = pack2(u[m][H + 2 * i], u[m][H + 2 * i + 1]);
+                            if (a.rot > 0) {
+                                const f32x2 c = pack2(turn.c[m][2 * i], turn.c[m][2 * i + 1]);
+                                const f32x2 sn = pack2(turn.s[m][2 * i], turn.s[m][2 * i + 1]);
+                                const f32x2 ns = pack2(-turn.s[m][2 * i], -turn.s[m][2 * i + 1]);
+                                const f32x2 y = fma2(u1[m][i], c, mul2(u2[m][i], ns));
+                                u2[m][i] = fma2(u2[m][i], c, mul2(u1[m][i], sn));
+                                u1[m][i] = y;
+                            }
+                            x1[m][i] = mul2(x1[m][i], ri2);
+                            x2[m][i] = mul2(x2[m][i], ri2);
+                            if (part) {      // rows that are not there are zero
+                                dw2[which][m][i] = fma2(u1[m][i], x1[m][i], dw2[which][m][i]);
+                                dw2[which][m][Q + i] = fma2(u2[m][i], x2[m][i], dw2[which][m][Q + i]);
+                            }
+                            u1[m][i] = mul2(u1[m][i], pack2(w[m][2 * i], w[m][2 * i + 1]));
+                            u2[m][i] = mul2(u2[m][i], pack2(w[m][H + 2 * i], w[m][H + 2 * i + 1]));
+                            sum = fma2(u1[m][i], x1[m][i], sum);
+                            sum = fma2(u2[m][i], x2[m][i], sum);
+                        }
+                    const float dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(sum2(sum)) * scale;
+                    const f32x2 dot2 = pack2(dot, dot);
+#pragma unroll
+                    for (int m = 0; m < NV; ++m)
+#pragma unroll
+                        for (int i = 0; i < Q; ++i) {
+                            unpack2(mul2(ri2, fma2(x1[m][i], dot2, u1[m][i])), u[m][2 * i], u[m][2 * i + 1]);
+                            unpack2(mul2(ri2, fma2(x2[m][i], dot2, u2[m][i])), u[m][H + 2 * i], u[m][H + 2 * i + 1]);
+                        }
+                } else {
+                    float ss = 0.f, dot = 0.f;
+#pragma unroll
+                    for (int m = 0; m < NV; ++m) ss = fmaf(x[m][0], x[m][0], ss);
+                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss), scale);
+                    if (a.rot > 0) turn.apply(u, lane, stage);
+#pragma unroll
+                    for (int m = 0; m < NV; ++m) {
+                        x[m][0] *= ri;
+                        dw[which][m] = fmaf(u[m][0], x[m][0], dw[which][m]);
+                        u[m][0] *= w[m][0];
+                        dot = fmaf(u[m][0], x[m][0], dot);
                     }
-                    if (there && h + r < last) {
+                    dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(dot) * scale;
 #pragma unroll
-                        for (int m = 0; m < NV; ++m) {
-                            if (!live)
+                    for (int m = 0; m < NV; ++m) u[m][0] = ri * fmaf(x[m][0], dot, u[m][0]);
+                }
+                if (there) {
 #pragma unroll
-                                for (int i = 0; i < V; ++i) u[m][i] = 0.f;
-                            if ((lane + m * LANES) * V < a.d) F::st(po + r * to.sh + m * LANES * V, u[m]);
-                        }
+                    for (int m = 0; m < NV; ++m) {
+                        if (!live)
+#pragma unroll
+                            for (int i = 0; i < V; ++i) u[m][i] = 0.f;
+                        if ((lane + m * LANES) * V < a.d) F::st(po, typename F::Place(lane + m * LANES, a.rot), u[m]);
                     }
                 }
-                po += kRows * to.sh;
+                po += to.sh;
             }
         }
+        copy_wait<0>();
     }
     if (!part) return;
     // the block's sums, lane group by lane group in order
@@ -360,12 +514,16 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_bwd_kernel(falcon_qknorm_
         if (slot == k) {
 #pragma unroll
             for (int m = 0; m < NV; ++m) {
-                const int e = (lane + m * LANES) * V;
-                if (e < a.d)
+                const int p = lane + m * LANES;
+                if (p * V < a.d)
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        sw[0][e + i] += dw[0][m][i];
-                        sw[1][e + i] += dw[1][m][i];
+                        const int e = R::channel(p, i, a.rot);
+                        float lo[2], hi[2];
+                        unpack2(dw2[0][m][i / 2 % NP], lo[0], hi[0]);
+                        unpack2(dw2[1][m][i / 2 % NP], lo[1], hi[1]);
+                        sw[0][e] += V == 1 ? dw[0][m] : i & 1 ? hi[0] : lo[0];
+                        sw[1][e] += V == 1 ? dw[1][m] : i & 1 ? hi[1] : lo[1];
                     }
             }
         }
@@ -375,13 +533,13 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_bwd_kernel(falcon_qknorm_
         part[(long long)blockIdx.x * 2 * a.d + i] = sw[i / a.d][i % a.d];
 }
 
-// The pack's width: 16 bytes of the io type where every row and the rotation allow it.
+// The pack's width: 16 bytes of the io type where every row and the rotation allow it (accesses are of half a pack).
 int norm_pack(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g) {
-    const int es = a.io_dtype == FALCON_BF16 ? 2 : 4, V = 16 / es;
-    bool ok = a.d % V == 0 && view_packs(a.q, V, es) && view_packs(a.k, V, es);
-    if (a.rot_layout == FALCON_ROT_HALF) ok = ok && (a.rot / 2) % V == 0;
-    if (!g) ok = ok && view_packs(a.q_out, V, es) && view_packs(a.k_out, V, es);
-    else ok = ok && view_packs(g->dq_out, 4, 4) && view_packs(g->dk_out, 4, 4) && view_packs(g->dq, 4, 4) && view_packs(g->dk, 4, 4);
+    const int es = a.io_dtype == FALCON_BF16 ? 2 : 4, V = 16 / es, H = V / 2;
+    bool ok = a.d % V == 0 && view_packs(a.q, H, es) && view_packs(a.k, H, es);
+    if (a.rot_layout == FALCON_ROT_HALF) ok = ok && a.rot % V == 0;
+    if (!g) ok = ok && view_packs(a.q_out, H, es) && view_packs(a.k_out, H, es);
+    else ok = ok && view_packs(g->dq_out, H, 4) && view_packs(g->dk_out, H, 4) && view_packs(g->dq, H, 4) && view_packs(g->dk, H, 4);
     return ok ? V : 1;
 }
 
@@ -393,7 +551,7 @@ int norm_lanes(const falcon_qknorm_args_t &a, int V) {
 // One token for each group of lanes; its heads over several groups while those are fewer than kWanted
 // threads (three quarters of what the GPU holds).
 NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
-    constexpr long long kWanted = 148LL * 1536;   // threads
+    constexpr long long kWanted = 148LL * 1536;
     NormShape s;
     const int heads = a.Hq + a.Hk, per = kNormThreads / lanes;
     const long long all = (long long)a.B * a.T;
@@ -407,14 +565,18 @@ NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
     return s;
 }
 
-constexpr long long kBwdBlocks = 148 * 4;
+constexpr long long kBwdBlocks = 148 * 2;   // what the SMs hold at once: the parts of dwq and dwk are few
 long long bwd_blocks(const NormShape &s) { return s.groups * s.parts < kBwdBlocks ? s.groups * s.parts : kBwdBlocks; }
 
 template <typename IO, int V, int LANES, int NV, bool HALF>
 cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
     const NormShape s = norm_shape(a, LANES);
-    const size_t smem = (size_t)(kNormThreads / LANES) * turn_slots(a, V) * sizeof(float2);
+    size_t smem = norm_turn_bytes(a, V, kNormThreads / LANES);
     if (g) {
+        if (V > 1) smem += (size_t)norm_ring(V, NV) * NV * kNormThreads * V * (sizeof(IO) + sizeof(float));
+        const cudaError_t e = cudaFuncSetAttribute(qknorm_bwd_kernel<IO, V, LANES, NV, HALF>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
         qknorm_bwd_kernel<IO, V, LANES, NV, HALF><<<(unsigned)bwd_blocks(s), kNormThreads, smem, st>>>(a, *g, s, part);
     } else {
         if (s.groups > kMaxGrid || s.parts > 65535) return cudaErrorInvalidConfiguration;

@@ -361,11 +361,15 @@ def falcon_decode_step(S, k_prev, q, k, v, alpha, eta, *, rule="falcon1", eps=1e
 # device, which need not be the current one. Outputs and workspaces that a call makes are allocated on
 # `stream` (default: the device's current stream), where its kernels run.
 
+_NO_VIEW = (None, 0, 0, 0)
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev, stream):
     """The context in which a call allocates, and the raw stream on which it launches."""
     if stream is None:
-        ctx = contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        return ctx, torch.cuda.current_stream(dev).cuda_stream
+        ctx = _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+        return ctx, torch._C._cuda_getCurrentRawStream(dev.index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     if stream.device != dev:
@@ -373,8 +377,15 @@ def _on(dev, stream):
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def _tensor(t, name, shape, dtype, dev):
-    """Refuses what is not a tensor of this shape, type and device."""
+def _rank(t, name, rank):
+    """The tensor that a call takes its device and type from."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != rank:
+        raise ValueError(f"{name} must have {rank} axes, got the shape {tuple(t.shape)}")
+
+
+def _refuse(t, name, shape, dtype, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -388,19 +399,21 @@ def _tensor(t, name, shape, dtype, dev):
 def _seq(t, name, shape, dtype, dev):
     """falcon_view_t of a (B, H, T, d) tensor, or of a (B, H, d) one as a single token."""
     if t is None:
-        return FalconView()
-    _tensor(t, name, shape, dtype, dev)
+        return _NO_VIEW
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, name, shape, dtype, dev)
     s = t.stride()
-    if shape[-1] > 1 and s[-1] != 1 and t.numel() > 0:
+    if s[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return FalconView(t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
+    return (t.data_ptr(), s[0], s[1], s[2] if len(s) == 4 else 0)
 
 
 def _arr(t, name, shape, dtype, dev):
     """Address of a contiguous parameter, state or gradient, or None."""
     if t is None:
         return None
-    _tensor(t, name, shape, dtype, dev)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -412,15 +425,8 @@ def _code(table, key, what) -> int:
     return table[key]
 
 
-def _rank(t, name, rank):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != rank:
-        raise ValueError(f"{name} must have {rank} axes, got the shape {tuple(t.shape)}")
-
-
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != FALCON_OK:
         raise FalconError(st, name)
 
@@ -437,19 +443,15 @@ def _workspace(workspace, need, dev):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _conv_args(x, w, bias, act, state, lengths, shape):
+def _conv_args(x, w, bias, act, state, lengths, shape, state_shape, y, state_out):
     dev, io, f32 = x.device, x.dtype, torch.float32
     B, H, d = shape[0], shape[1], shape[-1]
-    T = shape[2] if len(shape) == 4 else 1
-    _rank(w, "w", 3)
     K = w.shape[2]
-    a = FalconConvArgs(_dtype_code(x), B, H, T, d, K, _code(ACTS, act, "act"))
-    a.x = _seq(x, "x", shape, io, dev)
-    a.w = _arr(w, "w", (H, d, K), f32, dev)
-    a.bias = _arr(bias, "bias", (H, d), f32, dev)
-    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
-    a.state = _arr(state, "state", (B, H, max(K - 1, 0), d), io, dev)
-    return a, K
+    return FalconConvArgs(
+        _dtype_code(x), B, H, shape[2] if len(shape) == 4 else 1, d, K, _code(ACTS, act, "act"),
+        _seq(x, "x", shape, io, dev), _seq(y, "y", shape, io, dev), _arr(w, "w", (H, d, K), f32, dev),
+        _arr(bias, "bias", (H, d), f32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev),
+        _arr(state, "state", state_shape, io, dev), _arr(state_out, "state_out", state_shape, io, dev))
 
 
 def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=None, state_out=None,
@@ -459,16 +461,16 @@ def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=
     K - 1 inputs, made where want_state asks for it (it may be `state` itself). With ``lengths`` (B,)
     int32, rows of y behind a sequence's end are left as they were (uninitialised in a y made here)."""
     _rank(x, "x", 4)
-    a, K = _conv_args(x, w, bias, act, state, lengths, tuple(x.shape))
-    B, H, T, d = x.shape
+    _rank(w, "w", 3)
+    shape = B, H, T, d = tuple(x.shape)
+    tail = (B, H, max(w.shape[2] - 1, 0), d)
     ctx, raw = _on(x.device, stream)
     with ctx:
         if y is None:
-            y = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device)
+            y = torch.empty(shape, dtype=x.dtype, device=x.device)
         if state_out is None and want_state:
-            state_out = torch.empty((B, H, K - 1, d), dtype=x.dtype, device=x.device)
-        a.y = _seq(y, "y", (B, H, T, d), x.dtype, x.device)
-        a.state_out = _arr(state_out, "state_out", (B, H, K - 1, d), x.dtype, x.device)
+            state_out = torch.empty(tail, dtype=x.dtype, device=x.device)
+        a = _conv_args(x, w, bias, act, state, lengths, shape, tail, y, state_out)
         _call("falcon_conv_fwd", ctypes.byref(a), raw)
     return y, state_out
 
@@ -477,15 +479,14 @@ def falcon_conv_step(x, w, state, *, bias=None, act="silu", state_out=None, y=No
     """One token of the convolution for N sequences: x (N, H, d), state (N, H, K - 1, d), which is updated
     in place unless state_out is given. Returns y (N, H, d)."""
     _rank(x, "x", 3)
-    shape = tuple(x.shape)
-    a, K = _conv_args(x, w, bias, act, state, None, shape)
-    state_out = state if state_out is None else state_out
-    a.state_out = _arr(state_out, "state_out", (shape[0], shape[1], K - 1, shape[2]), x.dtype, x.device)
+    _rank(w, "w", 3)
+    shape = N, H, d = tuple(x.shape)
     ctx, raw = _on(x.device, stream)
     with ctx:
         if y is None:
             y = torch.empty(shape, dtype=x.dtype, device=x.device)
-        a.y = _seq(y, "y", shape, x.dtype, x.device)
+        a = _conv_args(x, w, bias, act, state, None, shape, (N, H, max(w.shape[2] - 1, 0), d), y,
+                       state if state_out is None else state_out)
         _call("falcon_conv_step", ctypes.byref(a), raw)
     return y
 
@@ -493,53 +494,53 @@ def falcon_conv_step(x, w, state, *, bias=None, act="silu", state_out=None, y=No
 def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None, dstate_out=None, dx=None,
                     workspace=None, stream=None):
     """Gradients of falcon_conv_fwd for dy (B, H, T, d) fp32 and dstate_out (B, H, K - 1, d) fp32 or None.
-    Returns a dict of fp32 tensors dx (in x's axis order, token-major like a projection's rows, unless given),
-    dw, dbias (None without bias) and dstate (None without state)."""
+    Returns a dict of fp32 tensors dx (token-major rows like a projection's, seen as (B, H, T, d), unless
+    given), dw, dbias (None without bias) and dstate (None without state)."""
     _rank(x, "x", 4)
+    _rank(w, "w", 3)
     f32, dev = torch.float32, x.device
-    a, K = _conv_args(x, w, bias, act, state, lengths, tuple(x.shape))
-    B, H, T, d = x.shape
+    shape = B, H, T, d = tuple(x.shape)
+    K = w.shape[2]
+    tail = (B, H, max(K - 1, 0), d)
     ctx, raw = _on(dev, stream)
     with ctx:
         if dx is None:
             dx = torch.empty((B, T, H, d), dtype=f32, device=dev).transpose(1, 2)
         out = {"dx": dx, "dw": torch.empty((H, d, K), dtype=f32, device=dev),
                "dbias": torch.empty((H, d), dtype=f32, device=dev) if bias is not None else None,
-               "dstate": torch.empty((B, H, K - 1, d), dtype=f32, device=dev) if state is not None else None}
-        g = FalconConvGrads()
-        g.dy = _seq(dy, "dy", (B, H, T, d), f32, dev)
-        g.dx = _seq(dx, "dx", (B, H, T, d), f32, dev)
-        g.dstate_out = _arr(dstate_out, "dstate_out", (B, H, K - 1, d), f32, dev)
-        g.dw, g.dbias, g.dstate = _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"])
-        need = int(lib().falcon_conv_bwd_workspace_size(ctypes.byref(a)))
+               "dstate": torch.empty(tail, dtype=f32, device=dev) if state is not None else None}
+        a = _conv_args(x, w, bias, act, state, lengths, shape, tail, None, None)
+        g = FalconConvGrads(_seq(dy, "dy", shape, f32, dev), _arr(dstate_out, "dstate_out", tail, f32, dev),
+                            _seq(dx, "dx", shape, f32, dev), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"]))
+        need = int((_lib or lib()).falcon_conv_bwd_workspace_size(ctypes.byref(a)))
         workspace, p, n = _workspace(workspace, need, dev)
         _call("falcon_conv_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
     return out
 
 
-def _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, step):
-    rank = 3 if step else 4
+def _scan_shapes(k, v, rank):
+    """(B, H, T, dk, dv), the shape of v and that of k."""
     _rank(v, "v", rank)
     _rank(k, "k", rank)
-    vs, ks = tuple(v.shape), tuple(k.shape)
+    vs = tuple(v.shape)
+    dk = k.shape[-1]
+    return (vs[0], vs[1], vs[2] if rank == 4 else 1, dk, vs[-1]), vs, vs[:-1] + (dk,)
+
+
+def _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, o, S_out):
+    B, H, T, dk, dv = sizes
     dev, io, f32 = v.device, v.dtype, torch.float32
-    B, H, dv, dk = vs[0], vs[1], vs[-1], ks[-1]
-    T = 1 if step else vs[2]
-    ks = vs[:-1] + (dk,)
-    a = FalconScanArgs(_dtype_code(v), B, H, T, dk, dv, FALCON_SCAN_SOFTPLUS if softplus else 0)
-    a.q, a.k = _seq(q, "q", ks, io, dev), _seq(k, "k", ks, io, dev)
-    a.v, a.delta = _seq(v, "v", vs, io, dev), _seq(delta, "delta", vs, io, dev)
-    a.z = _seq(z, "z", vs, io, dev)
-    a.A = _arr(A, "A", (H, dv, dk), f32, dev)
-    a.D = _arr(D, "D", (H, dv), f32, dev)
-    a.delta_bias = _arr(delta_bias, "delta_bias", (H, dv), f32, dev)
-    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
-    a.S0 = _arr(S0, "S0", (B, H, dv, dk), f32, dev)
-    return a, (B, H, T, dk, dv)
+    state = (B, H, dv, dk)
+    return FalconScanArgs(
+        _dtype_code(v), B, H, T, dk, dv, FALCON_SCAN_SOFTPLUS if softplus else 0, _seq(q, "q", ks, io, dev),
+        _seq(k, "k", ks, io, dev), _seq(v, "v", vs, io, dev), _seq(delta, "delta", vs, io, dev), _seq(z, "z", vs, io, dev),
+        _seq(o, "o", vs, io, dev), _arr(A, "A", (H, dv, dk), f32, dev), _arr(D, "D", (H, dv), f32, dev),
+        _arr(delta_bias, "delta_bias", (H, dv), f32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev),
+        _arr(S0, "S0", state, f32, dev), _arr(S_out, "S_out", state, f32, dev))
 
 
 def falcon_scan_workspace_size(args: FalconScanArgs) -> int:
-    return int(lib().falcon_scan_workspace_size(ctypes.byref(args)))
+    return int((_lib or lib()).falcon_scan_workspace_size(ctypes.byref(args)))
 
 
 def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softplus=True, S0=None, lengths=None,
@@ -547,16 +548,16 @@ def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softp
     """Selective scan: q, k (B, H, T, dk), v, delta and z (B, H, T, dv), A (H, dv, dk), D and delta_bias
     (H, dv), S0 (B, H, dv, dk); parameters and states fp32. Returns (o, S_out). With few channels the
     sequence is split, for which a workspace is made here unless one is given (a smaller one runs it whole)."""
-    a, (B, H, T, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, False)
+    sizes, vs, ks = _scan_shapes(k, v, 4)
+    B, H, T, dk, dv = sizes
     dev = v.device
     ctx, raw = _on(dev, stream)
     with ctx:
         if o is None:
-            o = torch.empty((B, H, T, dv), dtype=v.dtype, device=dev)
+            o = torch.empty(vs, dtype=v.dtype, device=dev)
         if S_out is None and want_state:
             S_out = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
-        a.o = _seq(o, "o", (B, H, T, dv), v.dtype, dev)
-        a.S_out = _arr(S_out, "S_out", (B, H, dv, dk), torch.float32, dev)
+        a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, o, S_out)
         workspace, p, n = _workspace(workspace, falcon_scan_workspace_size(a) if workspace is None else 0, dev)
         _call("falcon_scan_fwd", ctypes.byref(a), p, n, raw)
     return o, S_out
@@ -566,14 +567,12 @@ def falcon_scan_step(q, k, v, delta, A, S, *, D=None, z=None, delta_bias=None, s
                      stream=None):
     """One token of the scan for N sequences: q, k (N, H, dk), v, delta, z (N, H, dv); S (N, H, dv, dk) fp32 is
     updated in place unless S_out is given. Returns o (N, H, dv)."""
-    a, (B, H, _, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, None, S, True)
-    dev = v.device
-    a.S_out = _arr(S if S_out is None else S_out, "S_out", (B, H, dv, dk), torch.float32, dev)
-    ctx, raw = _on(dev, stream)
+    sizes, vs, ks = _scan_shapes(k, v, 3)
+    ctx, raw = _on(v.device, stream)
     with ctx:
         if o is None:
-            o = torch.empty((B, H, dv), dtype=v.dtype, device=dev)
-        a.o = _seq(o, "o", (B, H, dv), v.dtype, dev)
+            o = torch.empty(vs, dtype=v.dtype, device=v.device)
+        a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, None, S, o, S if S_out is None else S_out)
         _call("falcon_scan_step", ctypes.byref(a), raw)
     return o
 
@@ -583,7 +582,8 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
     """Gradients of falcon_scan_fwd for dO (B, H, T, dv) fp32 and dS_T (B, H, dv, dk) fp32 or None. Returns a
     dict of fp32 tensors dq, dk, dv, ddelta, dA and, for the inputs that were given, dD, ddelta_bias, dz, dS0
     (None otherwise). Sequence gradients are token-major rows seen as (B, H, T, d)."""
-    a, (B, H, T, dk, dv) = _scan_args(q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, False)
+    sizes, vs, ks = _scan_shapes(k, v, 4)
+    B, H, T, dk, dv = sizes
     dev, f32 = v.device, torch.float32
     ctx, raw = _on(dev, stream)
     with ctx:
@@ -594,41 +594,37 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
                "dD": torch.empty((H, dv), dtype=f32, device=dev) if D is not None else None,
                "ddelta_bias": torch.empty((H, dv), dtype=f32, device=dev) if delta_bias is not None else None,
                "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if S0 is not None else None}
-        g = FalconScanGrads()
-        g.dO = _seq(dO, "dO", (B, H, T, dv), f32, dev)
-        g.dS_T = _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev)
-        for n, d in (("dq", dk), ("dk", dk), ("dv", dv), ("ddelta", dv), ("dz", dv)):
-            setattr(g, n, _seq(out[n], n, (B, H, T, d), f32, dev))
-        for n in ("dA", "dD", "ddelta_bias", "dS0"):
-            setattr(g, n, _ptr(out[n]))
-        need = int(lib().falcon_scan_bwd_workspace_size(ctypes.byref(a)))
+        a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, None, None)
+        g = FalconScanGrads(_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev),
+                            *(_seq(out[n], n, s, f32, dev) for n, s in (("dq", ks), ("dk", ks), ("dv", vs), ("ddelta", vs), ("dz", vs))),
+                            *(_ptr(out[n]) for n in ("dA", "dD", "ddelta_bias", "dS0")))
+        need = int((_lib or lib()).falcon_scan_bwd_workspace_size(ctypes.byref(a)))
         workspace, p, n = _workspace(workspace, need, dev)
         _call("falcon_scan_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
     return out
 
 
-def _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths):
-    """q or k may be None (no heads of it)."""
+def _qknorm_shapes(q, k):
+    """The tensor that is there (q or k may be None: no heads of it), and the shapes of q and k."""
     x = q if q is not None else k
     if x is None:
         raise TypeError("q or k must be given")
     for t, n in ((q, "q"), (k, "k")):
         if t is not None:
             _rank(t, n, 4)
-    dev, io, f32 = x.device, x.dtype, torch.float32
     B, _, T, d = x.shape
-    qs = (B, q.shape[1] if q is not None else 0, T, d)
-    ks = (B, k.shape[1] if k is not None else 0, T, d)
+    return x, (B, q.shape[1] if q is not None else 0, T, d), (B, k.shape[1] if k is not None else 0, T, d)
+
+
+def _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, freq, positions, lengths):
+    dev, io, f32 = x.device, x.dtype, torch.float32
+    B, Hq, T, d = qs
     rot = int(rot)
-    a = FalconQknormArgs(_dtype_code(x), B, qs[1], ks[1], T, d, _code(NORMS, norm, "norm"), rot,
-                         _code(ROTS, layout, "layout"))
-    a.q, a.k = _seq(q, "q", qs, io, dev), _seq(k, "k", ks, io, dev)
-    a.wq, a.wk = _arr(wq, "wq", (d,), f32, dev), _arr(wk, "wk", (d,), f32, dev)
-    a.eps = float(eps)
-    a.freq = _arr(freq, "freq", (rot // 2,), f32, dev)
-    a.positions = _arr(positions, "positions", (B, T), torch.int32, dev)
-    a.lengths = _arr(lengths, "lengths", (B,), torch.int32, dev)
-    return a, qs, ks
+    return FalconQknormArgs(
+        _dtype_code(x), B, Hq, ks[1], T, d, _code(NORMS, norm, "norm"), rot, _code(ROTS, layout, "layout"),
+        _seq(q, "q", qs, io, dev), _seq(k, "k", ks, io, dev), _seq(q_out, "q_out", qs, io, dev), _seq(k_out, "k_out", ks, io, dev),
+        _arr(wq, "wq", (d,), f32, dev), _arr(wk, "wk", (d,), f32, dev), float(eps), _arr(freq, "freq", (rot // 2,), f32, dev),
+        _arr(positions, "positions", (B, T), torch.int32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev))
 
 
 def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, layout="half", freq=None, positions=None,
@@ -636,15 +632,14 @@ def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, la
     """Norm of each head's rows of q (B, Hq, T, d) and k (B, Hk, T, d) with the rotation of their first ``rot``
     channels by positions (B, T) int32 (default: 0, 1, ..) times freq (rot / 2) fp32. Either of q and k may be
     None. Returns (q_out, k_out), head-major unless given; q_out may be q itself, k_out k."""
-    a, qs, ks = _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
-    x = q if q is not None else k
+    x, qs, ks = _qknorm_shapes(q, k)
     ctx, raw = _on(x.device, stream)
     with ctx:
         if q_out is None and q is not None:
             q_out = torch.empty(qs, dtype=x.dtype, device=x.device)
         if k_out is None and k is not None:
             k_out = torch.empty(ks, dtype=x.dtype, device=x.device)
-        a.q_out, a.k_out = _seq(q_out, "q_out", qs, x.dtype, x.device), _seq(k_out, "k_out", ks, x.dtype, x.device)
+        a = _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
         _call("falcon_qknorm_fwd", ctypes.byref(a), raw)
     return q_out, k_out
 
@@ -654,19 +649,19 @@ def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps
     """Gradients of falcon_qknorm_fwd for dq_out, dk_out (fp32, the shapes of q and k). Returns a dict of fp32
     tensors dq, dk (token-major rows seen as (B, H, T, d); None where q or k is), dwq and dwk (None without
     the weight)."""
-    a, qs, ks = _qknorm_args(q, k, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
-    dev, f32 = (q if q is not None else k).device, torch.float32
+    x, qs, ks = _qknorm_shapes(q, k)
+    dev, f32 = x.device, torch.float32
     ctx, raw = _on(dev, stream)
     with ctx:
         rows = lambda s: torch.empty((s[0], s[2], s[1], s[3]), dtype=f32, device=dev).transpose(1, 2)
         out = {"dq": rows(qs) if q is not None else None, "dk": rows(ks) if k is not None else None,
                "dwq": torch.empty(qs[3:], dtype=f32, device=dev) if wq is not None else None,
                "dwk": torch.empty(qs[3:], dtype=f32, device=dev) if wk is not None else None}
-        g = FalconQknormGrads()
-        g.dq_out, g.dk_out = _seq(dq_out, "dq_out", qs, f32, dev), _seq(dk_out, "dk_out", ks, f32, dev)
-        g.dq, g.dk = _seq(out["dq"], "dq", qs, f32, dev), _seq(out["dk"], "dk", ks, f32, dev)
-        g.dwq, g.dwk = _ptr(out["dwq"]), _ptr(out["dwk"])
-        need = int(lib().falcon_qknorm_bwd_workspace_size(ctypes.byref(a))) if wq is not None or wk is not None else 0
+        a = _qknorm_args(x, qs, ks, q, k, None, None, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
+        g = FalconQknormGrads(_seq(dq_out, "dq_out", qs, f32, dev), _seq(dk_out, "dk_out", ks, f32, dev),
+                              _seq(out["dq"], "dq", qs, f32, dev), _seq(out["dk"], "dk", ks, f32, dev),
+                              _ptr(out["dwq"]), _ptr(out["dwk"]))
+        need = int((_lib or lib()).falcon_qknorm_bwd_workspace_size(ctypes.byref(a))) if wq is not None or wk is not None else 0
         workspace, p, n = _workspace(workspace, need, dev)
         _call("falcon_qknorm_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
     return out
