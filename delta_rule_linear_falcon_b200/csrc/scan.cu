@@ -253,82 +253,133 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
     }
 }
 
-// One token. A channel's row of the state is read and written by G lanes, four columns each, so the
-// state moves in whole lines; each thread has kStepRows channels' rows in flight.
+// One token. A channel's row of the state is read and written by G lanes, four columns each, so the state
+// moves in whole lines; each thread has the rows of kStepRows channels in flight, and those of the next sequence
+// while it works on this one's. A block takes the same channels of several sequences: A, as large as a sequence's
+// state, is read once for them. A channel's scalars (step, dt v, output) belong to one of its lanes.
 constexpr int kStepThreads = 128, kStepRows = 4;
 
 template <typename IO, int G, bool V4>
-__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_args_t a, int ngrp) {
-    constexpr int CPP = kStepThreads / G;   // channels of a pass
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_args_t a, int ngrp, int chunk) {
+    constexpr int CPP = kStepThreads / G;                          // channels of a pass
+    constexpr int OWN = G >= kStepRows ? 1 : kStepRows / G;        // rows whose scalars this lane keeps
     const int grp = blockIdx.x % (unsigned)ngrp;
-    const int bh = blockIdx.x / (unsigned)ngrp;
-    const int b = bh / a.H, h = bh % a.H;
-    const int sl = threadIdx.x % G, c0 = sl * 4;
+    const unsigned rest = blockIdx.x / (unsigned)ngrp;
+    const int h = rest % (unsigned)a.H;
+    const int b0 = (int)(rest / (unsigned)a.H) * chunk, b1 = min(b0 + chunk, a.B);
+    const int lane = threadIdx.x & 31, sl = threadIdx.x % G, c0 = sl * 4;
     const int ch0 = grp * CPP * kStepRows + threadIdx.x / G;
-    const IO *pq = row_of<IO>(a.q, b, h, 0), *pk = row_of<IO>(a.k, b, h, 0);
-    const IO *pv = row_of<IO>(a.v, b, h, 0), *pd = row_of<IO>(a.delta, b, h, 0);
-    const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, 0) : nullptr;
-    IO *po = row_of<IO>(a.o, b, h, 0);
-    const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0;
+    const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0, cols = c0 < a.dk;
+    // the row whose total lanes_sum leaves in this lane, and the lane of the group that keeps row i
+    const int own = G >= kStepRows ? sl / (G / kStepRows > 0 ? G / kStepRows : 1) : sl * OWN;
+    const bool writes = G < kStepRows || sl % (G / kStepRows > 0 ? G / kStepRows : 1) == 0;
+    auto keeper = [](int i) { return G >= kStepRows ? i * (G / kStepRows) : i / OWN; };
 
     auto row4 = [&](const float *p, float (&x)[4]) {
         if (V4) {
-            const float4 f = *reinterpret_cast<const float4 *>(p + c0);
+            const float4 f = __ldcs(reinterpret_cast<const float4 *>(p + c0));
             x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
         } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = c0 + r < a.dk ? p[c0 + r] : 0.f;
+            for (int r = 0; r < 4; ++r) x[r] = c0 + r < a.dk ? __ldcs(p + c0 + r) : 0.f;
         }
     };
-    float S[kStepRows][4], A[kStepRows][4], q[4], k[4];
-    const bool cols = c0 < a.dk;
+    float S[kStepRows][4], A2[kStepRows][4], q[4], k[4], raw[OWN], v[OWN], z[OWN], bias[OWN], skip[OWN];
+    auto fetch = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < kStepRows; ++i) {
-        const int ch = ch0 + i * CPP;
+        for (int i = 0; i < kStepRows; ++i) {
+            const int ch = ch0 + i * CPP;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) { S[i][r] = 0.f; A[i][r] = 0.f; }
-        if (ch < a.dv && cols) {
-            row4(a.S0 + ((long long)bh * a.dv + ch) * a.dk, S[i]);
-            row4(a.A + ((long long)h * a.dv + ch) * a.dk, A[i]);
+            for (int r = 0; r < 4; ++r) S[i][r] = 0.f;
+            if (ch < a.dv && cols) row4(a.S0 + (((long long)b * a.H + h) * a.dv + ch) * a.dk, S[i]);
         }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const bool in = c0 + r < a.dk;
-        q[r] = in ? Io<IO>::ld(pq, c0 + r) : 0.f;
-        k[r] = in ? Io<IO>::ld(pk, c0 + r) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kStepRows; ++i) {
-        const int ch = ch0 + i * CPP;
-        const bool ok = ch < a.dv;
-        const long long hc = (long long)h * a.dv + ch;
-        float dt = 0.f, v = 0.f;
-        if (ok) {
-            v = Io<IO>::ld(pv, ch);
-            dt = Io<IO>::ld(pd, ch) + (a.delta_bias ? a.delta_bias[hc] : 0.f);
-            if (soft) dt = softplus(dt);
-        }
-        float y = 0.f;
+        const IO *pq = row_of<IO>(a.q, b, h, 0), *pk = row_of<IO>(a.k, b, h, 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            S[i][r] = fmaf(fast_ex2(dt * (A[i][r] * kLog2e)), S[i][r], dt * v * k[r]);
-            y = fmaf(S[i][r], q[r], y);
+            q[r] = c0 + r < a.dk ? Io<IO>::ld(pq, c0 + r) : 0.f;
+            k[r] = c0 + r < a.dk ? Io<IO>::ld(pk, c0 + r) : 0.f;
         }
 #pragma unroll
-        for (int m = 1; m < G; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-        if (ok && cols) {
-            float *to = a.S_out + ((long long)bh * a.dv + ch) * a.dk + c0;
-            if (V4) *reinterpret_cast<float4 *>(to) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
-            else
+        for (int j = 0; j < OWN; ++j) {
+            const int ch = ch0 + (own + j) * CPP;
+            raw[j] = v[j] = z[j] = 0.f;
+            if (ch < a.dv) {
+                raw[j] = Io<IO>::ld(row_of<IO>(a.delta, b, h, 0), ch);
+                v[j] = Io<IO>::ld(row_of<IO>(a.v, b, h, 0), ch);
+                if (a.z.p) z[j] = Io<IO>::ld(row_of<IO>(a.z, b, h, 0), ch);
+            }
+        }
+    };
+    fetch(b0);
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const int ch = ch0 + i * CPP;
+        const float *row = a.A + ((long long)h * a.dv + ch) * a.dk + c0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) A2[i][r] = 0.f;
+        if (ch < a.dv && cols) {
+            if (V4) {
+                const float4 f = *reinterpret_cast<const float4 *>(row);
+                A2[i][0] = f.x * kLog2e; A2[i][1] = f.y * kLog2e; A2[i][2] = f.z * kLog2e; A2[i][3] = f.w * kLog2e;
+            } else {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (c0 + r < a.dk) to[r] = S[i][r];
+                    if (c0 + r < a.dk) A2[i][r] = row[r] * kLog2e;
+            }
         }
-        if (ok && sl == 0) {
-            if (a.D) y = fmaf(a.D[hc], v, y);
-            if (pz) y *= silu(Io<IO>::ld(pz, ch));
-            Io<IO>::st(po, ch, y);
+    }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        const int ch = ch0 + (own + j) * CPP;
+        bias[j] = ch < a.dv && a.delta_bias ? a.delta_bias[(long long)h * a.dv + ch] : 0.f;
+        skip[j] = ch < a.dv && a.D ? a.D[(long long)h * a.dv + ch] : 0.f;
+    }
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        float dt[OWN], dtv[OWN], vv[OWN], zz[OWN], y[kStepRows], T[kStepRows][4];
+#pragma unroll
+        for (int j = 0; j < OWN; ++j) {
+            const float x = raw[j] + bias[j];
+            dt[j] = soft ? softplus(x) : x;
+            dtv[j] = dt[j] * v[j];
+            vv[j] = v[j];
+            zz[j] = z[j];
+        }
+#pragma unroll
+        for (int i = 0; i < kStepRows; ++i) {
+            const float d = __shfl_sync(0xffffffffu, dt[i % OWN], keeper(i), G), x = __shfl_sync(0xffffffffu, dtv[i % OWN], keeper(i), G);
+            y[i] = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                T[i][r] = fmaf(fast_ex2(d * A2[i][r]), S[i][r], x * k[r]);
+                y[i] = fmaf(T[i][r], q[r], y[i]);
+            }
+        }
+        if (b + 1 < b1) fetch(b + 1);
+        const long long bh = (long long)b * a.H + h;
+#pragma unroll
+        for (int i = 0; i < kStepRows; ++i) {
+            const int ch = ch0 + i * CPP;
+            if (ch < a.dv && cols) {
+                float *to = a.S_out + (bh * a.dv + ch) * a.dk + c0;
+                if (V4) __stcs(reinterpret_cast<float4 *>(to), make_float4(T[i][0], T[i][1], T[i][2], T[i][3]));
+                else
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (c0 + r < a.dk) __stcs(to + r, T[i][r]);
+            }
+        }
+        bool first;
+        lanes_sum<kStepRows, G, 1>(y, lane, first);
+        if (writes) {
+            IO *po = row_of<IO>(a.o, b, h, 0);
+#pragma unroll
+            for (int j = 0; j < OWN; ++j) {
+                const int ch = ch0 + (own + j) * CPP;
+                float o = fmaf(skip[j], vv[j], y[j]);
+                if (a.z.p) o *= silu(zz[j]);
+                if (ch < a.dv) Io<IO>::st(po, ch, o);
+            }
         }
     }
 }
@@ -360,11 +411,13 @@ template <typename IO, int G>
 cudaError_t scan_step_t(const falcon_scan_args_t &a, cudaStream_t s) {
     const int per = kStepThreads / G * kStepRows;
     const int ngrp = (a.dv + per - 1) / per;
-    const long long blocks = (long long)ngrp * a.B * a.H;
+    int chunk = 8;   // sequences of a block, while two blocks a place on the GPU are left
+    while (chunk > 1 && (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk) < 148 * 8) chunk /= 2;
+    const long long blocks = (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk);
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.S0) | reinterpret_cast<uintptr_t>(a.S_out) | reinterpret_cast<uintptr_t>(a.A);
-    if (a.dk % 4 == 0 && any % 16 == 0) scan_step_kernel<IO, G, true><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp);
-    else scan_step_kernel<IO, G, false><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp);
+    if (a.dk % 4 == 0 && any % 16 == 0) scan_step_kernel<IO, G, true><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp, chunk);
+    else scan_step_kernel<IO, G, false><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp, chunk);
     return cudaGetLastError();
 }
 
