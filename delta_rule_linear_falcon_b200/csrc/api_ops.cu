@@ -111,6 +111,9 @@ falcon_status_t check_conv_out(const falcon_conv_args_t *a) {
 
 // ---- scan
 
+// The scan's kernels take token strides of up to 2^28 elements (32 bits of bytes).
+bool far_tokens(const falcon_view_t &v, int T) { return v.p && T > 1 && v.st > (1LL << 28); }
+
 falcon_status_t check_scan(const falcon_scan_args_t *a) {
     FALCON_NEED(a);
     FALCON_NEED(a->dk > 0);
@@ -125,6 +128,7 @@ falcon_status_t check_scan(const falcon_scan_args_t *a) {
     FALCON_TRY(check_view(a->v, a->B, a->H, a->T, a->dv, es, false));
     FALCON_TRY(check_view(a->delta, a->B, a->H, a->T, a->dv, es, false));
     if (a->z.p) FALCON_TRY(check_view(a->z, a->B, a->H, a->T, a->dv, es, false));
+    if (far_tokens(a->v, a->T) || far_tokens(a->delta, a->T) || far_tokens(a->z, a->T)) return FALCON_ERR_UNSUPPORTED;
     FALCON_NEED(ok_array(a->A, (long long)a->B * a->H > 0) && ok_array(a->D, false) && ok_array(a->delta_bias, false));
     FALCON_NEED(ok_array(a->lengths, false) && ok_array(a->S0, false));
     return FALCON_OK;
@@ -132,6 +136,7 @@ falcon_status_t check_scan(const falcon_scan_args_t *a) {
 
 falcon_status_t check_scan_out(const falcon_scan_args_t *a) {
     FALCON_TRY(check_view(a->o, a->B, a->H, a->T, a->dv, elem_size(a->io_dtype), true));
+    if (far_tokens(a->o, a->T)) return FALCON_ERR_UNSUPPORTED;
     FALCON_NEED(ok_array(a->S_out, false));
     return FALCON_OK;
 }
@@ -263,6 +268,7 @@ falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *a, const falcon_scan_g
     FALCON_TRY(check_view(g->dk, a->B, a->H, a->T, a->dk, 4, true));
     FALCON_TRY(check_view(g->dv, a->B, a->H, a->T, a->dv, 4, true));
     FALCON_TRY(check_view(g->ddelta, a->B, a->H, a->T, a->dv, 4, true));
+    if (far_tokens(g->dO, a->T)) return FALCON_ERR_UNSUPPORTED;
     if (g->dz.p) {
         FALCON_NEED(a->z.p);
         FALCON_TRY(check_view(g->dz, a->B, a->H, a->T, a->dv, 4, true));

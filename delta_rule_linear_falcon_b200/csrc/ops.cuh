@@ -44,6 +44,15 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t u, float &lo, float &hi) 
     lo = __uint_as_float(u << 16);
     hi = __uint_as_float(u & 0xffff0000u);
 }
+template <> struct Pack<__nv_bfloat16, 2> {
+    typedef uint32_t raw;
+    static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint32_t *>(p); }
+    static __device__ __forceinline__ raw zero() { return 0u; }
+    static __device__ __forceinline__ void cvt(raw r, float (&x)[2]) { unpack_bf16x2(r, x[0], x[1]); }
+    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[2]) {
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(x[0], x[1]);
+    }
+};
 template <> struct Pack<__nv_bfloat16, 4> {
     typedef uint2 raw;
     static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint2 *>(p); }
@@ -148,10 +157,54 @@ __device__ __forceinline__ f32x2 ex2_2(f32x2 a) {
     unpack2(a, lo, hi);
     return pack2(fast_ex2(lo), fast_ex2(hi));
 }
+// The same on the multiply-add pipes, for kernels that the exponential unit bounds: x = n + f with n the nearest
+// whole number (the low bits of x + 1.5 2^23), 2^f by a polynomial of degree 5 on [-1/2, 1/2] with constant 1 (a
+// least-squares fit reweighted towards equal errors: 2e-7 of the value with its roundings, as good as the unit's, and
+// exact towards f = 0), n added to the exponent. For x <= 0; below -125 the value is 2^-125.
+__device__ __forceinline__ f32x2 ex2_poly2(f32x2 a) {
+    float lo, hi;
+    unpack2(a, lo, hi);
+    const f32x2 x = pack2(fmaxf(lo, -125.f), fmaxf(hi, -125.f));
+    const f32x2 t = add2(x, pack2(12582912.f, 12582912.f));
+    const f32x2 f = fma2(add2(t, pack2(-12582912.f, -12582912.f)), pack2(-1.f, -1.f), x);
+    f32x2 p = fma2(f, pack2(0.0013264726f, 0.0013264726f), pack2(0.009671513f, 0.009671513f));
+    p = fma2(f, p, pack2(0.055507336f, 0.055507336f));
+    p = fma2(f, p, pack2(0.24022242f, 0.24022242f));
+    p = fma2(f, p, pack2(0.693147f, 0.693147f));
+    p = fma2(f, p, pack2(1.f, 1.f));
+    float pl, ph, tl, th;
+    unpack2(p, pl, ph);
+    unpack2(t, tl, th);
+    return pack2(__int_as_float(__float_as_int(pl) + (__float_as_int(tl) << 23)),
+                 __int_as_float(__float_as_int(ph) + (__float_as_int(th) << 23)));
+}
 __device__ __forceinline__ float sum2(f32x2 a) {
     float lo, hi;
     unpack2(a, lo, hi);
     return lo + hi;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// softplus and x / (1 + e^-x) of two values.
+__device__ __forceinline__ f32x2 softplus2(f32x2 x) {
+    float a, b, c, d;
+    unpack2(x, a, b);
+    const float ea = fast_ex2(-1.4426950408889634f * fabsf(a)), eb = fast_ex2(-1.4426950408889634f * fabsf(b));
+    const f32x2 e = pack2(ea, eb);
+    unpack2(add2(e, pack2(2.f, 2.f)), c, d);
+    const f32x2 s = mul2(e, pack2(fast_rcp(c), fast_rcp(d))), u = mul2(s, s), s2 = add2(s, s);
+    f32x2 p = fma2(u, pack2(0.14005996f, 0.14005996f), pack2(0.14000902f, 0.14000902f));
+    p = fma2(u, p, pack2(0.20010763f, 0.20010763f));
+    p = fma2(u, p, pack2(0.33333209f, 0.33333209f));
+    return add2(pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)), fma2(mul2(s2, u), p, s2));
+}
+__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+    float a, b;
+    unpack2(add2(ex2_2(mul2(x, pack2(-1.4426950408889634f, -1.4426950408889634f))), pack2(1.f, 1.f)), a, b);
+    return mul2(x, pack2(fast_rcp(a), fast_rcp(b)));
 }
 // Four floats of a 16-byte aligned row as two pairs.
 __device__ __forceinline__ void load_pairs(const float *p, f32x2 &a, f32x2 &b) {

@@ -5,12 +5,14 @@
 // Each entry of the state takes one exponential and four fp32 operations a token, so at dk = 16 the
 // exponential unit (16 a clock and SM) bounds the pass, well above HBM: 16 exponentials against about
 // eight bytes of v, delta, z and o. No product is shared between channels, so there is no matrix
-// instruction to use. A thread owns a channel and ST <= 16 columns of its state in registers (SL lanes
-// share a channel when dk > 16 and join their parts of o); neighbouring lanes own neighbouring channels,
-// so v, delta, z and o move as whole lines whatever their alignment. q_t and k_t are the same for all
-// channels of a head: the block stages kScanChunk tokens of them in shared memory (double buffered) and
-// reads them as broadcasts. The next chunk's loads are issued before this chunk's arithmetic.
-// The step size (softplus) is computed once per channel and token, 1 / 16 of the state's exponentials.
+// instruction to use. A thread owns a channel and ST <= 16 columns of its state in registers, two columns an
+// instruction (SL lanes share a channel when dk > 16 and join their parts of o). Everything else is kept short,
+// because it competes with those exponentials for the instruction slots: v, delta and z of kScanChunk tokens come
+// as 16-byte asynchronous copies into a ring in shared memory, one copy a thread and tensor, and are read there at
+// fixed offsets; o goes back the same way, in the place of z (or v) (loads and stores of single elements, with
+// their addresses, took a fifth of the pass). Where rows are not 16-byte multiples, elements are copied one by one.
+// q_t and k_t, the same for all channels of a head, are staged in fp32 and read as broadcasts. Step sizes (softplus)
+// are computed two tokens an instruction, once per channel and token.
 //
 // Split: B H dv channels are the only parallel axis of the recurrence; with few of them the sequence is
 // cut into segments (scan_plan). A first launch runs every segment from a zero state and leaves its end
@@ -22,15 +24,77 @@ namespace falcon {
 
 namespace {
 
-template <typename IO, int ST, int SL, int MODE>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a, ScanWork w, int ngrp) {
+// Rows of CHUNK tokens x CPB channels of E, brought into shared memory by the block's threads. WIDE: asynchronous
+// copies of 16 bytes; otherwise a thread holds its elements in registers between load() and store().
+template <typename E, int CPB, bool WIDE> struct Tile {
+    static constexpr int kPer = 16 / (int)sizeof(E);                       // elements of a copy
+    static constexpr int kPieces = kScanChunk * CPB / kPer;
+    static constexpr int kCopies = (kPieces + kScanThreads - 1) / kScanThreads;
+    static constexpr int kElems = (kScanChunk * CPB + kScanThreads - 1) / kScanThreads;
+    E raw[WIDE ? 1 : kElems];
+    // the rows t.. of `view` from channel c0 on, te tokens and dv channels being there
+    __device__ __forceinline__ void load(E *to, const E *rows, long long st, int left, int channels) {
+        if (WIDE) {
+#pragma unroll
+            for (int m = 0; m < kCopies; ++m) {
+                const int p = threadIdx.x + m * kScanThreads, j = p / (CPB / kPer), c = p % (CPB / kPer) * kPer;
+                if (p < kPieces && j < left && c < channels) copy_async<16>(to + j * CPB + c, rows + j * st + c);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < kElems; ++m) {
+                const int p = threadIdx.x + m * kScanThreads, j = p / CPB, c = p % CPB;
+                if (p < kScanChunk * CPB && j < left && c < channels) raw[m] = rows[j * st + c];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(E *to) const {
+        if (!WIDE) {
+#pragma unroll
+            for (int m = 0; m < kElems; ++m) {
+                const int p = threadIdx.x + m * kScanThreads;
+                if (p < kScanChunk * CPB) to[p] = raw[m];
+            }
+        }
+    }
+};
+
+// CHUNK tokens' outputs from shared memory to their rows, by the threads that copied those places in.
+template <typename E, int CPB, bool WIDE>
+__device__ __forceinline__ void put_rows(const E *from, E *rows, long long st, int left, int channels) {
+    typedef Tile<E, CPB, WIDE> T;
+    if (WIDE) {
+#pragma unroll
+        for (int m = 0; m < T::kCopies; ++m) {
+            const int p = threadIdx.x + m * kScanThreads, j = p / (CPB / T::kPer), c = p % (CPB / T::kPer) * T::kPer;
+            if (p < T::kPieces && j < left && c < channels)
+                *reinterpret_cast<uint4 *>(rows + j * st + c) = *reinterpret_cast<const uint4 *>(from + j * CPB + c);
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < T::kElems; ++m) {
+            const int p = threadIdx.x + m * kScanThreads, j = p / CPB, c = p % CPB;
+            if (p < kScanChunk * CPB && j < left && c < channels) rows[j * st + c] = from[p];
+        }
+    }
+}
+
+template <typename IO, int ST, int SL, int MODE, bool WIDE>
+__global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_kernel(falcon_scan_args_t a, ScanWork w, int ngrp) {
+    constexpr int C = kScanChunk;
     constexpr int DKP = ST * SL;                     // padded columns
     constexpr int CPB = kScanThreads / SL;           // channels of a block
     constexpr int ROW = 2 * DKP;                     // k and q of a token
-    constexpr int NKQ = (kScanChunk * ROW + kScanThreads - 1) / kScanThreads;
+    constexpr int NKQ = (C * ROW + kScanThreads - 1) / kScanThreads;
     constexpr int NP = ST / 2;                       // pairs of columns of a thread
+    // of the segments' ends pass, every fourth pair's exponentials go to the multiply-add pipes (3% of the whole split
+    // pass; with outputs, or more of them, the instruction slots are worth more)
+    constexpr int POLY = MODE == kScanEnds ? 4 : 0;
+    constexpr int RING = WIDE ? (sizeof(IO) == 4 ? 2 : 3) : 2;   // chunks in shared memory
     typedef Pack<IO, 1> P;
-    __shared__ __align__(16) float kq[2][kScanChunk * ROW];
+    __shared__ __align__(16) float kq[2][C * ROW];
+    __shared__ __align__(16) IO tv[RING][C * CPB], td[RING][C * CPB], tz[RING][MODE == kScanEnds ? 1 : C * CPB];
+    __shared__ __align__(16) float tg[RING][MODE == kScanBoth ? C * CPB : 1];
 
     unsigned bid = blockIdx.x;
     const int grp = (int)(bid % (unsigned)ngrp);
@@ -39,7 +103,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
     const int seg0 = (int)(bid / (unsigned)(a.B * a.H)) * (MODE == kScanBoth ? w.run : 1);
     const int b = bh / a.H, h = bh % a.H;
     const int tid = threadIdx.x;
-    const int sl = tid % SL, ch = grp * CPB + tid / SL;
+    const int sl = tid % SL, lc = tid / SL, ch = grp * CPB + lc;
+    const int channels = min(CPB, a.dv - grp * CPB);
     const bool ok = ch < a.dv;
     const int n = seq_length(a.lengths, b, a.T);
     // tokens [t0, t1), of which those below n are there
@@ -65,6 +130,60 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
         return;
     }
 
+    // ---- the ring: one tile for each tensor and chunk
+    const bool has_z = MODE != kScanEnds && a.z.p;
+    const long long c0 = (long long)grp * CPB;
+    const IO *pv = row_of<IO>(a.v, b, h, t0) + c0, *pd = row_of<IO>(a.delta, b, h, t0) + c0;
+    const IO *pz = has_z ? row_of<IO>(a.z, b, h, t0) + c0 : nullptr;
+    const float *pg = MODE == kScanBoth ? row_of<float>(w.dO, b, h, t0) + c0 : nullptr;
+    const IO *pk = row_of<IO>(a.k, b, h, 0), *pq = row_of<IO>(a.q, b, h, 0);
+    Tile<IO, CPB, WIDE> xv, xd, xz;
+    Tile<float, CPB, WIDE> xg;
+    auto ask = [&](int t, int place) {   // the chunk at t; the row pointers go on to the next
+        if (t < te) {
+            xv.load(tv[place], pv, a.v.st, te - t, channels);
+            xd.load(td[place], pd, a.delta.st, te - t, channels);
+            if (has_z) xz.load(tz[place], pz, a.z.st, te - t, channels);
+            if (MODE == kScanBoth) xg.load(tg[place], pg, w.dO.st, te - t, channels);
+        }
+        pv += C * a.v.st;
+        pd += C * a.delta.st;
+        if (has_z) pz += C * a.z.st;
+        if (MODE == kScanBoth) pg += C * w.dO.st;
+        if (WIDE) copy_commit();
+    };
+    auto settle = [&](int place) {       // !WIDE: what ask() holds in registers
+        xv.store(tv[place]);
+        xd.store(td[place]);
+        if (has_z) xz.store(tz[place]);
+        if (MODE == kScanBoth) xg.store(tg[place]);
+    };
+    typename P::raw rkq[NKQ];
+    auto load_kq = [&](int t) {
+#pragma unroll
+        for (int m = 0; m < NKQ; ++m) {
+            const int e = tid + m * kScanThreads, j = e / ROW, c = e % DKP;
+            const bool isq = e % ROW >= DKP;
+            rkq[m] = P::zero();
+            if (e < C * ROW && t + j < te && c < a.dk && !(MODE == kScanEnds && isq))
+                rkq[m] = isq ? P::ld(pq + (t + j) * a.q.st + c) : P::ld(pk + (t + j) * a.k.st + c);
+        }
+    };
+    auto stage_kq = [&](float *to) {
+#pragma unroll
+        for (int m = 0; m < NKQ; ++m) {
+            const int e = tid + m * kScanThreads;
+            float x[1];
+            P::cvt(rkq[m], x);
+            if (e < C * ROW) to[e] = x[0];
+        }
+    };
+    load_kq(t0);
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) ask(t0 + i * C, i);
+    if (!WIDE) settle(0);
+
+    // ---- this thread's state
     f32x2 A2[NP], S[NP], Pr[MODE == kScanBoth ? NP : 1], G[MODE == kScanBoth ? NP : 1];
     auto column = [&](const float *row, int s) { return ok && row && sl * ST + s < a.dk ? row[sl * ST + s] : 0.f; };
 #pragma unroll
@@ -98,87 +217,56 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
         }
     }
 
-    const unsigned cu = ok ? (unsigned)ch : 0u;
-    const IO *pv = row_of<IO>(a.v, b, h, t0), *pd = row_of<IO>(a.delta, b, h, t0);
-    const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, t0) : nullptr;
-    const IO *pk = row_of<IO>(a.k, b, h, 0), *pq = row_of<IO>(a.q, b, h, 0);
-    const float *pg = MODE == kScanBoth ? row_of<float>(w.dO, b, h, t0) : nullptr;
-    IO *po = MODE == kScanFull ? row_of<IO>(a.o, b, h, t0) : nullptr;
-
-    typename P::raw rv[kScanChunk], rd[kScanChunk], rz[kScanChunk], rkq[NKQ];
-    float rg[MODE == kScanBoth ? kScanChunk : 1];
-    // loads of the chunk at t, and the row pointers on to the next one
-    auto fetch = [&](int t) {
-        const bool whole = t + kScanChunk <= te;
-#pragma unroll
-        for (int j = 0; j < kScanChunk; ++j) {
-            const bool in = whole || t + j < te;
-            rv[j] = P::zero();
-            rd[j] = P::zero();
-            if (MODE != kScanEnds) rz[j] = P::zero();
-            if (MODE == kScanBoth) rg[j] = 0.f;
-            if (in) {
-                rv[j] = P::ld(pv + cu);
-                rd[j] = P::ld(pd + cu);
-                if (MODE != kScanEnds && pz) rz[j] = P::ld(pz + cu);
-                if (MODE == kScanBoth) rg[j] = pg[cu];
-            }
-            pv += a.v.st;
-            pd += a.delta.st;
-            if (MODE != kScanEnds && pz) pz += a.z.st;
-            if (MODE == kScanBoth) pg += w.dO.st;
-        }
-#pragma unroll
-        for (int m = 0; m < NKQ; ++m) {
-            const int e = tid + m * kScanThreads, j = e / ROW, c = e % DKP;
-            const bool isq = e % ROW >= DKP;
-            rkq[m] = P::zero();
-            if (e < kScanChunk * ROW && t + j < te && c < a.dk && !(MODE == kScanEnds && isq))
-                rkq[m] = isq ? P::ld(pq + (t + j) * a.q.st + c) : P::ld(pk + (t + j) * a.k.st + c);
-        }
-    };
-
+    IO *po = MODE == kScanFull ? row_of<IO>(a.o, b, h, t0) + c0 : nullptr;
     float sum = 0.f;
     int seg = seg0, left = w.seg;   // kScanBoth: the segment being walked and its tokens to come
-    fetch(t0);
-    int buf = 0;
-    for (int t = t0; t < (MODE == kScanBoth ? t1 : te); t += kScanChunk, buf ^= 1) {
-        float dt[kScanChunk], v[kScanChunk], z[kScanChunk], g[kScanChunk];
-#pragma unroll
-        for (int m = 0; m < NKQ; ++m) {
-            const int e = tid + m * kScanThreads;
-            float x[1];
-            P::cvt(rkq[m], x);
-            if (e < kScanChunk * ROW) kq[buf][e] = x[0];
+    const int tend = MODE == kScanBoth ? t1 : te;
+    int place = 0, before = RING - 1, buf = 0;
+    for (int t = t0; t < tend; t += C, buf ^= 1) {
+        stage_kq(kq[buf]);
+        if (WIDE) copy_wait<RING - 2>();
+        __syncthreads();   // the chunk is there, and the one before is through
+        if (MODE == kScanFull && t > t0) {
+            put_rows<IO, CPB, WIDE>(has_z ? tz[before] : tv[before], po, a.o.st, C, channels);
+            po += C * a.o.st;
+            if (!WIDE) __syncthreads();   // other threads' elements
         }
+        load_kq(t + C);
+        ask(t + (RING - 1) * C, before);
+
+        float dt[C], g[C];
+        const IO *const vs = tv[place] + lc, *const ds = td[place] + lc;
+        IO *const zs = tz[place] + (MODE == kScanEnds ? 0 : lc);
 #pragma unroll
-        for (int j = 0; j < kScanChunk; ++j) {
-            float x[1];
-            P::cvt(rv[j], x);
-            v[j] = x[0];
-            P::cvt(rd[j], x);
-            const float raw = x[0] + bias;
-            dt[j] = soft ? softplus(raw) : raw;
-            if (MODE != kScanEnds) {
-                P::cvt(rz[j], x);
-                z[j] = x[0];
+        for (int j = 0; j < C; j += 2) {
+            const float x0 = Io<IO>::ld(ds, j * CPB) + bias, x1 = Io<IO>::ld(ds, (j + 1) * CPB) + bias;
+            dt[j] = x0;
+            dt[j + 1] = x1;
+            if (soft) unpack2(softplus2(pack2(x0, x1)), dt[j], dt[j + 1]);
+            g[j] = g[j + 1] = 0.f;
+            if (MODE == kScanBoth) {
+                const float *const gs = tg[place] + lc;
+                g[j] = gs[j * CPB];
+                g[j + 1] = gs[(j + 1) * CPB];
+                if (has_z)
+                    unpack2(mul2(pack2(g[j], g[j + 1]), silu2(pack2(Io<IO>::ld(zs, j * CPB), Io<IO>::ld(zs, (j + 1) * CPB)))), g[j], g[j + 1]);
             }
-            g[j] = MODE == kScanBoth ? (pz ? rg[j] * silu(z[j]) : rg[j]) : 0.f;
         }
-        if (t + kScanChunk > te) {   // behind the end the step is 0, the state stays, and nothing flows back
+        const bool whole = t + C <= te;
+        if (!whole) {   // behind the end the step is 0, the state stays, and nothing flows back
 #pragma unroll
-            for (int j = 0; j < kScanChunk; ++j)
-                if (t + j >= te) dt[j] = v[j] = g[j] = 0.f;
+            for (int j = 0; j < C; ++j)
+                if (t + j >= te) dt[j] = g[j] = 0.f;
         }
-        if (t + kScanChunk < te) fetch(t + kScanChunk);
-        __syncthreads();   // the chunk is staged; the other buffer was last read before this barrier
-        const bool whole = t + kScanChunk <= te;
+        float y[C];
 #pragma unroll
-        for (int j = 0; j < kScanChunk; ++j) {
+        for (int j = 0; j < C; ++j) {
             const float *k4 = &kq[buf][j * ROW + sl * ST];
             const float *q4 = &kq[buf][j * ROW + DKP + sl * ST];
             const f32x2 dt2 = pack2(dt[j], dt[j]);
-            const float b1 = dt[j] * v[j];
+            float v = Io<IO>::ld(vs, j * CPB);
+            if (!whole && t + j >= te) v = 0.f;   // the ring holds anything there
+            const float b1 = dt[j] * v;
             const f32x2 b2 = pack2(b1, b1);
             f32x2 y2 = 0ull, g2 = 0ull;
             if (MODE == kScanBoth) g2 = pack2(g[j], g[j]);
@@ -190,7 +278,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
                 if (MODE != kScanEnds) load_pairs(q4 + 2 * s, qq[0], qq[1]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const f32x2 e = ex2_2(mul2(dt2, A2[s + r]));
+                    const f32x2 x = mul2(dt2, A2[s + r]);
+                    const f32x2 e = POLY > 0 && (s + r) % (POLY > 0 ? POLY : 1) == 0 ? ex2_poly2(x) : ex2_2(x);
                     S[s + r] = fma2(e, S[s + r], mul2(b2, kk[r]));
                     if (MODE == kScanFull) y2 = fma2(S[s + r], qq[r], y2);
                     if (MODE == kScanBoth) {
@@ -200,27 +289,34 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
                 }
             }
             if (MODE == kScanFull) {
-                float y = sum2(y2);
+                y[j] = sum2(y2);
 #pragma unroll
-                for (int m = 1; m < SL; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-                y = fmaf(skip, v[j], y);
-                if (pz) y *= silu(z[j]);
-                if (ok && sl == 0 && (whole || t + j < te)) {
-                    const float out[1] = {y};
-                    P::st(po + cu, out);
-                }
-                po += a.o.st;
+                for (int m = 1; m < SL; m <<= 1) y[j] += __shfl_xor_sync(0xffffffffu, y[j], m);
+                y[j] = fmaf(skip, v, y[j]);
             }
         }
+        if (MODE == kScanFull && sl == 0) {   // outputs in the place of z, or of v
+            IO *const os = has_z ? zs : tv[place] + lc;
+#pragma unroll
+            for (int j = 0; j < C; j += 2) {
+                if (has_z)
+                    unpack2(mul2(pack2(y[j], y[j + 1]), silu2(pack2(Io<IO>::ld(zs, j * CPB), Io<IO>::ld(zs, (j + 1) * CPB)))), y[j], y[j + 1]);
+                Io<IO>::st(os, j * CPB, y[j]);
+                Io<IO>::st(os, (j + 1) * CPB, y[j + 1]);
+            }
+        }
+        before = place;
+        place = place + 1 < RING ? place + 1 : 0;
+        if (!WIDE) settle(place);
         if (MODE == kScanBoth) {
-            left -= kScanChunk;
-            if (left == 0 || t + kScanChunk >= t1) {   // the segment's end: hand it over, start the next from zero
+            left -= C;
+            if (left == 0 || t + C >= t1) {   // the segment's end: hand it over, start the next from zero
                 if (ok) {
-                    float *const to = ends + (long long)seg * DKP, *const tg = w.grads + (bhc * w.nseg + seg) * DKP + sl * ST;
+                    float *const to = ends + (long long)seg * DKP, *const tg_ = w.grads + (bhc * w.nseg + seg) * DKP + sl * ST;
 #pragma unroll
                     for (int s = 0; s < NP; s += 2) {
                         store_pairs(to + 2 * s, S[s], S[s + 1]);
-                        store_pairs(tg + 2 * s, G[s], G[s + 1]);
+                        store_pairs(tg_ + 2 * s, G[s], G[s + 1]);
                     }
                     if (sl == 0) steps[seg] = sum;
                 }
@@ -235,6 +331,11 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(falcon_scan_args_t a
                 }
             }
         }
+    }
+    if (WIDE) copy_wait<0>();
+    if (MODE == kScanFull && tend > t0) {   // the last chunk's outputs
+        __syncthreads();
+        put_rows<IO, CPB, WIDE>(has_z ? tz[before] : tv[before], po, a.o.st, (te - t0 - 1) % C + 1, channels);
     }
     if (MODE == kScanBoth || !ok) return;
     if (MODE == kScanEnds) {
@@ -384,27 +485,37 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_arg
     }
 }
 
-template <typename IO, int ST, int SL>
-cudaError_t scan_pass_t(int mode, const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
+template <typename IO, int ST, int SL, int MODE>
+cudaError_t scan_pass_t(const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
     const int cpb = kScanThreads / SL;
     const int ngrp = (a.dv + cpb - 1) / cpb;
-    const int runs = mode == kScanBoth ? (w.nseg + w.run - 1) / w.run : w.nseg;
+    const int runs = MODE == kScanBoth ? (w.nseg + w.run - 1) / w.run : w.nseg;
     const long long blocks = (long long)ngrp * a.B * a.H * runs;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
-    if (mode == kScanFull) scan_kernel<IO, ST, SL, kScanFull><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
-    else if (mode == kScanEnds) scan_kernel<IO, ST, SL, kScanEnds><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
-    else scan_kernel<IO, ST, SL, kScanBoth><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
+    const int es = sizeof(IO), V = 16 / es;
+    bool wide = a.dv % V == 0 && view_packs(a.v, V, es) && view_packs(a.delta, V, es) && view_packs(a.z, V, es);
+    if (MODE == kScanFull) wide = wide && view_packs(a.o, V, es);
+    if (MODE == kScanBoth) wide = wide && view_packs(w.dO, 4, 4);
+    if (wide) scan_kernel<IO, ST, SL, MODE, true><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
+    else scan_kernel<IO, ST, SL, MODE, false><<<(unsigned)blocks, kScanThreads, 0, s>>>(a, w, ngrp);
     return cudaGetLastError();
+}
+
+template <typename IO, int ST, int SL>
+cudaError_t scan_pass_mode(int mode, const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
+    if (mode == kScanFull) return scan_pass_t<IO, ST, SL, kScanFull>(a, w, s);
+    if (mode == kScanEnds) return scan_pass_t<IO, ST, SL, kScanEnds>(a, w, s);
+    return scan_pass_t<IO, ST, SL, kScanBoth>(a, w, s);
 }
 
 template <typename IO>
 cudaError_t scan_pass_io(int mode, const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
-    if (a.dk <= 4) return scan_pass_t<IO, 4, 1>(mode, a, w, s);
-    if (a.dk <= 8) return scan_pass_t<IO, 8, 1>(mode, a, w, s);
-    if (a.dk <= 16) return scan_pass_t<IO, 16, 1>(mode, a, w, s);
-    if (a.dk <= 32) return scan_pass_t<IO, 16, 2>(mode, a, w, s);
-    if (a.dk <= 64) return scan_pass_t<IO, 16, 4>(mode, a, w, s);
-    return scan_pass_t<IO, 16, 8>(mode, a, w, s);
+    if (a.dk <= 4) return scan_pass_mode<IO, 4, 1>(mode, a, w, s);
+    if (a.dk <= 8) return scan_pass_mode<IO, 8, 1>(mode, a, w, s);
+    if (a.dk <= 16) return scan_pass_mode<IO, 16, 1>(mode, a, w, s);
+    if (a.dk <= 32) return scan_pass_mode<IO, 16, 2>(mode, a, w, s);
+    if (a.dk <= 64) return scan_pass_mode<IO, 16, 4>(mode, a, w, s);
+    return scan_pass_mode<IO, 16, 8>(mode, a, w, s);
 }
 
 template <typename IO, int G>
@@ -437,21 +548,35 @@ cudaError_t launch_scan_pass(int mode, const falcon_scan_args_t &a, const ScanWo
     return a.io_dtype == FALCON_BF16 ? scan_pass_io<__nv_bfloat16>(mode, a, w, s) : scan_pass_io<float>(mode, a, w, s);
 }
 
-// Segments: as many as fill the SMs with kWarpsWanted warps each, of at least kMinSeg tokens, and only
-// where the unsplit grid has less than half of that (the split costs the exponentials twice).
+// Segments: the number with the shortest estimate. A token takes a block alone on its SM 1.75 times what it takes
+// one of several (measured at dk = 16: 380 cycles against 219 for each), so k blocks on an SM take max(1.75, k) a token.
+// Both passes over a segment of L tokens are 1.8 L tokens' work (the first forms no outputs) and each join of a
+// state before it about one. Unsplit, the pass is T tokens' work.
 ScanPlan scan_plan(const falcon_scan_args_t &a, int num_sms) {
-    constexpr long long kWarpsWanted = 12, kMinSeg = 64;
+    constexpr long long kMinSeg = 32;
     ScanPlan p;
     p.seg = a.T;
     const int sl = a.dk <= 16 ? 1 : a.dk <= 32 ? 2 : a.dk <= 64 ? 4 : 8;
-    const long long bh = (long long)a.B * a.H;
-    const long long warps = bh * ((a.dv * (long long)sl + kScanThreads - 1) / kScanThreads) * (kScanThreads / 32);
-    const long long want = kWarpsWanted * num_sms;
-    if (warps == 0 || warps * 2 > want) return p;
-    long long nseg = want / warps;
-    const long long most = a.T / kMinSeg;
-    if (nseg > most) nseg = most;
-    if (nseg < 3) return p;
+    const long long bh = (long long)a.B * a.H, cpb = kScanThreads / sl;
+    const long long groups = bh * ((a.dv + cpb - 1) / cpb);
+    if (groups == 0 || a.T < 2 * kMinSeg) return p;
+    auto token = [&](long long blocks) {
+        const long long k = (blocks + num_sms - 1) / num_sms;
+        return k <= 1 ? 1.75 : (double)k;
+    };
+    double best = (double)a.T * token(groups);
+    long long nseg = 1;
+    for (int k = 1; k <= 8; ++k) {
+        long long n = (long long)num_sms * k / groups;
+        if (n > a.T / kMinSeg) n = a.T / kMinSeg;
+        if (n < 2) continue;
+        const double cost = (1.8 * (double)a.T / n + 0.5 * n) * token(groups * n);
+        if (cost < best) {
+            best = cost;
+            nseg = n;
+        }
+    }
+    if (nseg == 1) return p;
     long long seg = (a.T + nseg - 1) / nseg;
     seg = (seg + kScanChunk - 1) / kScanChunk * kScanChunk;
     p.seg = (int)seg;
