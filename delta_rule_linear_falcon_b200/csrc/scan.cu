@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
     const int grp = (int)(bid % (unsigned)ngrp);
     bid /= (unsigned)ngrp;
     const int bh = (int)(bid % (unsigned)(a.B * a.H));
-    const int seg0 = (int)(bid / (unsigned)(a.B * a.H)) * (MODE == kScanBoth ? w.run : 1);
+    const int seg0 = (int)(bid / (unsigned)(a.B * a.H)) * (MODE == kScanBoth ? w.walk * w.block : 1);
     const int b = bh / a.H, h = bh % a.H;
     const int tid = threadIdx.x;
     const int sl = tid % SL, lc = tid / SL, ch = grp * CPB + lc;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
     const int n = seq_length(a.lengths, b, a.T);
     // tokens [t0, t1), of which those below n are there
     const long long first = (long long)seg0 * w.seg;
-    const long long last = MODE == kScanBoth ? first + (long long)w.run * w.seg : first + w.seg;
+    const long long last = MODE == kScanBoth ? first + (long long)w.walk * w.block * w.seg : first + w.seg;
     const int t0 = (int)(first < a.T ? first : a.T);
     const int t1 = (int)(last < a.T ? last : a.T);
     const int te = n < t1 ? n : t1;
@@ -219,10 +219,20 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
 
     IO *po = MODE == kScanFull ? row_of<IO>(a.o, b, h, t0) + c0 : nullptr;
     float sum = 0.f;
-    int seg = seg0, left = w.seg;   // kScanBoth: the segment being walked and its tokens to come
+    int seg = seg0, left = 0;   // kScanBoth: the next segment, and the tokens before it
     const int tend = MODE == kScanBoth ? t1 : te;
     int place = 0, before = RING - 1, buf = 0;
     for (int t = t0; t < tend; t += C, buf ^= 1) {
+        if (MODE == kScanBoth && left == 0) {   // the state before the segment that starts here
+            if (ok) {
+                float *const to = ends + (long long)seg * DKP;
+#pragma unroll
+                for (int s = 0; s < NP; s += 2) store_pairs(to + 2 * s, S[s], S[s + 1]);
+                if (sl == 0) steps[seg] = sum;
+            }
+            ++seg;
+            left = w.seg;
+        }
         stage_kq(kq[buf]);
         if (WIDE) copy_wait<RING - 2>();
         __syncthreads();   // the chunk is there, and the one before is through
@@ -310,18 +320,17 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
         if (!WIDE) settle(place);
         if (MODE == kScanBoth) {
             left -= C;
-            if (left == 0 || t + C >= t1) {   // the segment's end: hand it over, start the next from zero
+            if (t + C >= t1 || (left == 0 && seg % w.walk == 0)) {   // the walk's end: hand it over, start the next from zero
                 if (ok) {
-                    float *const to = ends + (long long)seg * DKP, *const tg_ = w.grads + (bhc * w.nseg + seg) * DKP + sl * ST;
+                    const long long at = bhc * w.nwalk + (seg - 1) / w.walk;
+                    float *const to = w.wends + at * DKP + sl * ST, *const to_g = w.wgrads + at * DKP + sl * ST;
 #pragma unroll
                     for (int s = 0; s < NP; s += 2) {
                         store_pairs(to + 2 * s, S[s], S[s + 1]);
-                        store_pairs(tg_ + 2 * s, G[s], G[s + 1]);
+                        store_pairs(to_g + 2 * s, G[s], G[s + 1]);
                     }
-                    if (sl == 0) steps[seg] = sum;
+                    if (sl == 0) w.wsteps[at] = sum;
                 }
-                ++seg;
-                left = w.seg;
                 sum = 0.f;
 #pragma unroll
                 for (int s = 0; s < NP; ++s) {
@@ -489,7 +498,7 @@ template <typename IO, int ST, int SL, int MODE>
 cudaError_t scan_pass_t(const falcon_scan_args_t &a, const ScanWork &w, cudaStream_t s) {
     const int cpb = kScanThreads / SL;
     const int ngrp = (a.dv + cpb - 1) / cpb;
-    const int runs = MODE == kScanBoth ? (w.nseg + w.run - 1) / w.run : w.nseg;
+    const int runs = MODE == kScanBoth ? (w.nwalk + w.block - 1) / w.block : w.nseg;
     const long long blocks = (long long)ngrp * a.B * a.H * runs;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const int es = sizeof(IO), V = 16 / es;

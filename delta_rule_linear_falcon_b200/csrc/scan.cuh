@@ -14,18 +14,24 @@ constexpr int kScanChunk = 8;   // tokens whose inputs are loaded together
 enum ScanMode : int {
     kScanFull = 0,   // outputs, from the given or joined start state
     kScanEnds = 1,   // each segment's end state from a zero state, and its sum of steps
-    kScanBoth = 2    // the same, and the gradient that its outputs send to the state before it
+    kScanBoth = 2    // for the backward pass: walks of several segments, each from a zero state: the state before each
+                     // segment, the walk's end state, and the gradient that its outputs send to the state before it
 };
 
-// States between segments: [B,H,dv][nseg][cols], cols = dk rounded up to scan_cols (16-byte rows); the
-// segments of a channel lie together, so that the walk along them reads consecutive lines.
+// States between segments: [B,H,dv][number][cols], cols = dk rounded up to scan_cols (16-byte rows); those of a
+// channel lie together, so that the walk along them reads consecutive lines.
 struct ScanWork {
     int seg, nseg;     // tokens of a segment (a multiple of kScanChunk), segments
-    int run;           // segments that a block of kScanBoth walks
-    float *ends;       // end states (kScanEnds: the last segment's place keeps the initial state)
-    float *grads;      // kScanBoth
-    float *steps;      // [B,H,dv][nseg] sums of steps
-    falcon_view_t dO;  // kScanBoth
+    float *ends;       // kScanEnds: [nseg] end states (the last segment's place keeps the initial state);
+                       // kScanBoth: [nseg] states before the segments
+    float *steps;      // [B,H,dv][nseg] sums of steps: of the segment; kScanBoth: of its walk before it
+    // kScanBoth
+    int walk, nwalk;   // segments of a walk, walks
+    int block;         // walks of a block
+    float *wends;      // [nwalk] end states of the walks
+    float *wgrads;     // [nwalk] gradients with respect to the states before them
+    float *wsteps;     // [B,H,dv][nwalk] sums of steps
+    falcon_view_t dO;
 };
 
 inline int scan_cols(int dk) { return dk <= 4 ? 4 : dk <= 8 ? 8 : dk <= 16 ? 16 : dk <= 32 ? 32 : dk <= 64 ? 64 : 128; }

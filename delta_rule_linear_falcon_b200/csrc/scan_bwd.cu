@@ -2,15 +2,17 @@
 // dy_t = dO_t silu(z_t), G_t = dL/dS_t runs backwards, G_t = dy_t q_t^T + a_{t+1} G_{t+1}, and
 //   dq_t = sum_i dy S_t;  dk_t = sum_i G_t dt v;  sum_c G_t k -> dv, ddelta;
 //   W_t = G_t a_t S_{t-1}:  ddt += sum_c A W;  dA += dt W.
-// Both chains are linear, so the sequence is cut into segments of kSeg tokens that need nothing from each
-// other but S before and G behind them:
-//   1. every segment's end state from zero, its sum of steps, and the gradient that its outputs send to
-//      the state before it (sum_t prod_{s<=t} a_s dy_t q_t, one exponential for both directions);
-//   2. the joins along the segments, S ascending and G descending, in place;
-//   3. every segment on its own: S forward (dq, the output for dz, the state at every kSub-th token kept in
-//      shared memory), then, kSub tokens at a time, their states again into registers and G backward;
-//   4. sums of partial rows: dA, dD, ddelta_bias over segments and sequences, dq and dk over the blocks of
-//      a head's channels, in a fixed order.
+// Both chains are linear, so the sequence is cut into walks of a few segments of kSeg tokens, and walks need nothing
+// from each other but S before and G behind them:
+//   1. from a zero state before each walk: the state before each of its segments, its end state and sum of steps, and
+//      the gradient that its outputs send to the state before it (sum_t prod_{s<=t} a_s dy_t q_t, one exponential for
+//      both directions);
+//   2. the joins along the walks, S ascending and G descending, in place;
+//   3. every walk on its own, its segments from the last to the first, G handed down: S forward from the segment's
+//      state (dq, the output for dz, the state at every kSub-th token kept in shared memory), then, kSub tokens at a
+//      time, their states again into registers and G backward;
+//   4. sums of partial rows: dA, dD, ddelta_bias over walks and sequences, dq and dk over the blocks of a head's
+//      channels, in a fixed order.
 // Step 3 sums over channels (dq, dk) and over columns (dv, ddelta, dz) of the same products. A thread owns
 // 4 channels x 4 columns, SL = dk / 4 lanes side by side: the first additions of either sum are fused
 // multiply-adds in registers, the rest 3 to 6 shuffles (lanes_sum) for 16 entries.
@@ -23,7 +25,7 @@ namespace {
 constexpr int kSub = 4;              // tokens whose states are kept in registers
 constexpr int kNSub = 4;
 constexpr int kSeg = kSub * kNSub;   // tokens of a segment
-constexpr int kWalk = 8;             // segments that a block of step 1 walks
+constexpr int kBlockTokens = 64;     // tokens that a block of step 1 takes, or one walk
 
 template <int SL> struct BwdShape {
     static constexpr int kWarps = SL == 1 ? 1 : (SL == 2 ? 2 : 4);
@@ -41,46 +43,45 @@ template <int SL> struct BwdShape {
 };
 
 struct ScanBwdWork {
-    int nseg, nrun, run;           // segments; blocks along them in step 3, of `run` segments each
-    float *ends, *grads, *steps;   // as in ScanWork
-    float *dA;                     // [nrun][B][H,dv,dk] parts
-    float *dd, *db;                // [nrun][B][H,dv] parts of dD and ddelta_bias
+    ScanWork s;                    // seg = kSeg; wends and wgrads hold the joined states after step 2
+    float *dA;                     // [nwalk][B][H,dv,dk] parts
+    float *dd, *db;                // [nwalk][B][H,dv] parts of dD and ddelta_bias
     float *qk;                     // [2][ngrp][B,H,T,dk] parts of dq and dk (where a head has several blocks)
 };
 
 // Step 2. A thread per column of a channel's state: y = 0 walks the end states upwards and leaves the state
-// before each segment, y = 1 walks the gradients downwards and leaves the gradient behind each segment.
-__global__ void __launch_bounds__(256) scan_join_kernel(falcon_scan_args_t a, ScanBwdWork w, int cols, const float *dS_T, float *dS0) {
+// before each walk, y = 1 goes over the gradients downwards and leaves the gradient behind each walk.
+__global__ void __launch_bounds__(256) scan_join_kernel(falcon_scan_args_t a, ScanWork w, int cols, const float *dS_T, float *dS0) {
     const long long rows = (long long)a.B * a.H * a.dv;
     const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
     const long long row = e / cols;
     const int c = (int)(e % cols);
     if (row >= rows || c >= a.dk) return;
     const float A2 = a.A[row % ((long long)a.H * a.dv) * a.dk + c] * kLog2e;
-    const float *steps = w.steps + row * w.nseg;
-    constexpr int U = 16;   // segments in flight
+    const float *steps = w.wsteps + row * w.nwalk;
+    constexpr int U = 16;   // walks in flight
     if (blockIdx.y == 0) {
-        float *x = w.ends + row * w.nseg * cols + c;
+        float *x = w.wends + row * w.nwalk * cols + c;
         float S = a.S0 ? a.S0[row * a.dk + c] : 0.f;
-        for (int j0 = 0; j0 < w.nseg; j0 += U) {
+        for (int j0 = 0; j0 < w.nwalk; j0 += U) {
             float y[U], d[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (j0 + u < w.nseg) {
+                if (j0 + u < w.nwalk) {
                     y[u] = x[(long long)(j0 + u) * cols];
                     d[u] = steps[j0 + u];
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (j0 + u < w.nseg) {
+                if (j0 + u < w.nwalk) {
                     x[(long long)(j0 + u) * cols] = S;
                     S = fmaf(fast_ex2(A2 * d[u]), S, y[u]);
                 }
         }
     } else {
-        float *x = w.grads + row * w.nseg * cols + c;
+        float *x = w.wgrads + row * w.nwalk * cols + c;
         float G = dS_T ? dS_T[row * a.dk + c] : 0.f;
-        for (int j0 = w.nseg - 1; j0 >= 0; j0 -= U) {
+        for (int j0 = w.nwalk - 1; j0 >= 0; j0 -= U) {
             float y[U], d[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -118,7 +119,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
     const int grp = (int)(bid % (unsigned)ngrp);
     bid /= (unsigned)ngrp;
     const int bh = (int)(bid % (unsigned)(a.B * a.H));
-    const int runi = (int)(bid / (unsigned)(a.B * a.H));
+    const int walk = (int)(bid / (unsigned)(a.B * a.H));
     const int b = bh / a.H, h = bh % a.H;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sl = lane % SL, cl = lane / SL;
@@ -165,22 +166,26 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
             for (int s = 0; s < 4; ++s) S[i][s] = fma2(ex2_2(mul2(dt[i], A2[i][s])), S[i][s], mul2(dtv[i], k[s]));
     };
 
-    const int seg_end = min((runi + 1) * w.run, w.nseg);
+    const int seg0 = walk * w.s.walk, seg1 = min(seg0 + w.s.walk, w.s.nseg);
 #pragma unroll 1
-    for (int seg = runi * w.run; seg < seg_end; ++seg) {
+    for (int seg = seg1 - 1; seg >= seg0; --seg) {
         const int t0 = seg * kSeg;
         const int here = min(max(n - t0, 0), kSeg), rows = min(a.T - t0, kSeg);   // tokens of the sequence; of the arrays
-        // ---- the segment's states (one load per channel), then its inputs
+        // ---- the segment's states (a row of each channel), then its inputs
         {
-            f32x2 x[4][2], y[4][2];
+            f32x2 x[4][2], y[4][2], u[4][2];
+            float pre[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int ch = c00 + lc + i;
-                x[i][0] = x[i][1] = y[i][0] = y[i][1] = 0ull;
+                x[i][0] = x[i][1] = y[i][0] = y[i][1] = u[i][0] = u[i][1] = 0ull;
+                pre[i] = 0.f;
                 if (ch < a.dv) {
-                    const long long at = (((long long)bh * a.dv + ch) * w.nseg + seg) * COLS + sl * 4;
-                    load_pairs(w.ends + at, x[i][0], x[i][1]);
-                    load_pairs(w.grads + at, y[i][0], y[i][1]);
+                    const long long row = (long long)bh * a.dv + ch;
+                    load_pairs(w.s.ends + (row * w.s.nseg + seg) * COLS + sl * 4, x[i][0], x[i][1]);
+                    load_pairs(w.s.wends + (row * w.s.nwalk + walk) * COLS + sl * 4, y[i][0], y[i][1]);
+                    pre[i] = w.s.steps[row * w.s.nseg + seg];
+                    if (seg == seg1 - 1) load_pairs(w.s.wgrads + (row * w.s.nwalk + walk) * COLS + sl * 4, u[i][0], u[i][1]);
                 }
             }
             const IO *pk = row_of<IO>(a.k, b, h, t0), *pq = row_of<IO>(a.q, b, h, t0);
@@ -234,20 +239,29 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
                     }
                 }
             }
+            // rows of channels to pairs of channels; S = the walk's own part + the decayed state before the walk
+            auto turned = [](const f32x2 (&r)[4][2], f32x2 (&o)[2][4]) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    float p0, p1, r0, r1;
-                    unpack2(x[2 * i][s], p0, p1);
-                    unpack2(x[2 * i + 1][s], r0, r1);
-                    S[i][2 * s] = pack2(p0, r0);
-                    S[i][2 * s + 1] = pack2(p1, r1);
-                    unpack2(y[2 * i][s], p0, p1);
-                    unpack2(y[2 * i + 1][s], r0, r1);
-                    G[i][2 * s] = pack2(p0, r0);
-                    G[i][2 * s + 1] = pack2(p1, r1);
-                }
+                    for (int s = 0; s < 2; ++s) {
+                        float p0, p1, r0, r1;
+                        unpack2(r[2 * i][s], p0, p1);
+                        unpack2(r[2 * i + 1][s], r0, r1);
+                        o[i][2 * s] = pack2(p0, r0);
+                        o[i][2 * s + 1] = pack2(p1, r1);
+                    }
+            };
+            f32x2 before[2][4];
+            turned(x, S);
+            turned(y, before);
+            if (seg == seg1 - 1) turned(u, G);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x2 p2 = pack2(pre[2 * i], pre[2 * i + 1]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) S[i][s] = fma2(ex2_2(mul2(p2, A2[i][s])), before[i][s], S[i][s]);
+            }
         }
         __syncthreads();
 
@@ -441,7 +455,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
         __syncthreads();   // the next segment's inputs take these places
     }
     // ---- this block's parts of the parameters' gradients
-    const long long part = (long long)runi * a.B + b, HV = (long long)a.H * a.dv;
+    const long long part = (long long)walk * a.B + b, HV = (long long)a.H * a.dv;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -497,14 +511,14 @@ int bwd_channels(int sl) {
 }
 
 struct BwdSizes {
-    int nseg, run, nrun, ngrp, cols;
+    int nseg, walk, nwalk, ngrp, cols;
     long long rows;     // channels of all sequences
-    long long states;   // floats of all states between segments
     long long qk;       // floats of all parts of dq and dk
+    long long floats;   // the workspace
 };
 
-// Segments that a block of step 3 takes one after the other: its parts of dA (as large as the state) and its
-// prologue are shared by them; as many as leave four blocks for each place on an SM.
+// Segments of a walk: as many as leave four blocks of step 3 for each place on an SM. Long walks make few joins, and
+// few parts of dA (each as large as the state).
 BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     BwdSizes z;
     z.nseg = (a.T + kSeg - 1) / kSeg;
@@ -512,17 +526,17 @@ BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     z.ngrp = (a.dv + ch - 1) / ch;
     z.cols = scan_cols(a.dk);
     z.rows = (long long)a.B * a.H * a.dv;
-    z.states = z.nseg * z.rows * z.cols;
-    z.run = 1;
-    while (z.run < 16 && (long long)z.ngrp * a.B * a.H * ((z.nseg + 2 * z.run - 1) / (2 * z.run)) >= 148 * 12) z.run *= 2;
-    z.nrun = (z.nseg + z.run - 1) / z.run;
+    z.walk = 1;
+    while (z.walk < 16 && (long long)z.ngrp * a.B * a.H * ((z.nseg + 2 * z.walk - 1) / (2 * z.walk)) >= 148 * 12) z.walk *= 2;
+    z.nwalk = (z.nseg + z.walk - 1) / z.walk;
     z.qk = z.ngrp > 1 ? 2LL * z.ngrp * a.B * a.H * a.T * a.dk : 0;
+    z.floats = z.rows * (z.nseg * (z.cols + 1LL) + z.nwalk * (2LL * z.cols + 1 + a.dk + 2)) + z.qk;
     return z;
 }
 
 template <typename IO, int SL>
 cudaError_t scan_bwd_t(const falcon_scan_args_t &a, const falcon_scan_grads_t &g, const ScanBwdWork &w, int ngrp, cudaStream_t s) {
-    const long long blocks = (long long)ngrp * a.B * a.H * w.nrun;
+    const long long blocks = (long long)ngrp * a.B * a.H * w.s.nwalk;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const size_t smem = BwdShape<SL>::kBytes;
     cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<IO, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -545,42 +559,36 @@ cudaError_t scan_bwd_io(const falcon_scan_args_t &a, const falcon_scan_grads_t &
 
 }  // namespace
 
-size_t scan_bwd_workspace(const falcon_scan_args_t &a) {
-    const BwdSizes z = bwd_sizes(a);
-    return sizeof(float) * (size_t)(2 * z.states + z.nseg * z.rows + z.nrun * z.rows * (a.dk + 2) + z.qk);
-}
+size_t scan_bwd_workspace(const falcon_scan_args_t &a) { return sizeof(float) * (size_t)bwd_sizes(a).floats; }
 
 cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads_t &g, float *ws, cudaStream_t s) {
     if (a.H == 0) return cudaSuccess;
     const BwdSizes z = bwd_sizes(a);
     ScanBwdWork w{};
-    w.nseg = z.nseg;
-    w.nrun = z.nrun;
-    w.run = z.run;
-    w.ends = ws;   // the rows of states first: they are read as 16-byte pairs
-    w.grads = w.ends + z.states;
-    w.steps = w.grads + z.states;
-    w.dA = w.steps + z.nseg * z.rows;
-    w.dd = w.dA + z.nrun * z.rows * a.dk;
-    w.db = w.dd + z.nrun * z.rows;
-    w.qk = w.db + z.nrun * z.rows;
+    w.s.seg = kSeg;
+    w.s.nseg = z.nseg;
+    w.s.walk = z.walk;
+    w.s.nwalk = z.nwalk;
+    w.s.block = z.walk * kSeg >= kBlockTokens ? 1 : kBlockTokens / (z.walk * kSeg);
+    w.s.dO = g.dO;
+    w.s.ends = ws;   // the rows of states first: they are read as 16-byte pairs
+    w.s.wends = w.s.ends + z.nseg * z.rows * z.cols;
+    w.s.wgrads = w.s.wends + z.nwalk * z.rows * z.cols;
+    w.s.steps = w.s.wgrads + z.nwalk * z.rows * z.cols;
+    w.s.wsteps = w.s.steps + z.nseg * z.rows;
+    w.dA = w.s.wsteps + z.nwalk * z.rows;
+    w.dd = w.dA + z.nwalk * z.rows * a.dk;
+    w.db = w.dd + z.nwalk * z.rows;
+    w.qk = w.db + z.nwalk * z.rows;
     cudaError_t e;
     if (a.B > 0) {
         if (z.nseg > 0) {
-            ScanWork p{};
-            p.seg = kSeg;
-            p.nseg = z.nseg;
-            p.run = kWalk;
-            p.ends = w.ends;
-            p.grads = w.grads;
-            p.steps = w.steps;
-            p.dO = g.dO;
-            e = launch_scan_pass(kScanBoth, a, p, s);
+            e = launch_scan_pass(kScanBoth, a, w.s, s);
             if (e != cudaSuccess) return e;
         }
         const long long jb = (z.rows * z.cols + 255) / 256;
         if (jb > kMaxGrid) return cudaErrorInvalidConfiguration;
-        scan_join_kernel<<<dim3((unsigned)jb, 2), 256, 0, s>>>(a, w, z.cols, g.dS_T, g.dS0);
+        scan_join_kernel<<<dim3((unsigned)jb, 2), 256, 0, s>>>(a, w.s, z.cols, g.dS_T, g.dS0);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         if (z.nseg > 0) {
@@ -597,7 +605,7 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
     }
     const long long hrows = (long long)a.H * a.dv, hplane = hrows * a.dk;
     const SumJob jobs[3] = {{w.dA, hplane, hplane, g.dA}, {w.dd, hrows, hrows, g.dD}, {w.db, hrows, hrows, g.ddelta_bias}};
-    return launch_column_sums(jobs, 3, (long long)z.nrun * a.B, s);
+    return launch_column_sums(jobs, 3, (long long)z.nwalk * a.B, s);
 }
 
 }  // namespace falcon
