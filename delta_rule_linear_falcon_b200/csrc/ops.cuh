@@ -188,7 +188,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// softplus and x / (1 + e^-x) of two values.
+// softplus, 1 / (1 + e^-x) and x / (1 + e^-x) of two values.
 __device__ __forceinline__ f32x2 softplus2(f32x2 x) {
     float a, b, c, d;
     unpack2(x, a, b);
@@ -201,11 +201,12 @@ __device__ __forceinline__ f32x2 softplus2(f32x2 x) {
     p = fma2(u, p, pack2(0.33333209f, 0.33333209f));
     return add2(pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)), fma2(mul2(s2, u), p, s2));
 }
-__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 x) {
     float a, b;
     unpack2(add2(ex2_2(mul2(x, pack2(-1.4426950408889634f, -1.4426950408889634f))), pack2(1.f, 1.f)), a, b);
-    return mul2(x, pack2(fast_rcp(a), fast_rcp(b)));
+    return pack2(fast_rcp(a), fast_rcp(b));
 }
+__device__ __forceinline__ f32x2 silu2(f32x2 x) { return mul2(x, sigmoid2(x)); }
 // Four floats of a 16-byte aligned row as two pairs.
 __device__ __forceinline__ void load_pairs(const float *p, f32x2 &a, f32x2 &b) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);

@@ -106,6 +106,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
     typedef BwdShape<SL> Sh;
     typedef Pack<IO, 1> P;
     constexpr int NT = Sh::kThreads, CH = Sh::kCh, COLS = Sh::kCols, CL = 32 / SL;
+    constexpr int EU = 16;   // tokens whose loads are in flight at a segment's end
     extern __shared__ __align__(16) float sm[];
     float *sDt = sm;                    // [token][channel]: dt;  after its token: sum_c G k
     float *sDv = sDt + Sh::kChan;       // dt v;                  after its token: sum_c A W
@@ -228,14 +229,20 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
                         pg += g.dO.st;
                     }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int at = (j0 + u) * CH + cc;
-                        float dt = Io<IO>::cvt(rd[u]) + bias[m];
-                        if (soft) dt = softplus(dt);
-                        if (!(ok && j0 + u < here)) dt = 0.f;
-                        sDt[at] = dt;
-                        sDv[at] = dt * Io<IO>::cvt(rv[u]);
-                        sDy[at] = pz ? rg[u] * silu(Io<IO>::cvt(rz[u])) : rg[u];
+                    for (int u = 0; u < U; u += 2) {
+                        float *to = sDt + (j0 + u) * CH + cc;   // the arrays lie kChan apart
+                        float d0 = Io<IO>::cvt(rd[u]) + bias[m], d1 = Io<IO>::cvt(rd[u + 1]) + bias[m];
+                        if (soft) unpack2(softplus2(pack2(d0, d1)), d0, d1);
+                        if (!(ok && j0 + u < here)) d0 = 0.f;
+                        if (!(ok && j0 + u + 1 < here)) d1 = 0.f;
+                        float g0 = rg[u], g1 = rg[u + 1];
+                        if (pz) unpack2(mul2(pack2(g0, g1), silu2(pack2(Io<IO>::cvt(rz[u]), Io<IO>::cvt(rz[u + 1])))), g0, g1);
+                        to[0] = d0;
+                        to[CH] = d1;
+                        to[Sh::kChan] = d0 * Io<IO>::cvt(rv[u]);
+                        to[Sh::kChan + CH] = d1 * Io<IO>::cvt(rv[u + 1]);
+                        to[2 * Sh::kChan] = g0;
+                        to[2 * Sh::kChan + CH] = g1;
                     }
                 }
             }
@@ -372,64 +379,82 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
         }
         __syncthreads();
 
-        // ---- gradients of the channels
+        // ---- gradients of the channels, two tokens an instruction; the loads of all tokens are in flight together
 #pragma unroll
         for (int m = 0; m < Sh::kPer; ++m) {
             const int cc = tid + m * NT, ch = c00 + cc;
             if (cc >= CH || ch >= a.dv) continue;
             const IO *pv = row_of<IO>(a.v, b, h, t0) + ch, *pd = row_of<IO>(a.delta, b, h, t0) + ch;
-            const IO *pz = a.z.p ? row_of<IO>(a.z, b, h, t0) + ch : nullptr;
-            const float *pg = row_of<float>(g.dO, b, h, t0) + ch;
             float *ov = row_of<float>(g.dv, b, h, t0) + ch, *od = row_of<float>(g.ddelta, b, h, t0) + ch;
-            float *oz = pz && g.dz.p ? row_of<float>(g.dz, b, h, t0) + ch : nullptr;
-            constexpr int U = 8;
+            const bool has_dz = a.z.p && g.dz.p;
+            const IO *pz = has_dz ? row_of<IO>(a.z, b, h, t0) + ch : nullptr;
+            const float *pg = row_of<float>(g.dO, b, h, t0) + ch;
+            float *oz = has_dz ? row_of<float>(g.dz, b, h, t0) + ch : nullptr;
+            typename P::raw rv[EU], rd[EU], rz[EU];
+            float rg[EU];
 #pragma unroll 1
-            for (int j0 = 0; j0 < rows; j0 += U) {
-                typename P::raw rv[U], rd[U], rz[U];
-                float rg[U];
+            for (int j0 = 0; j0 < rows; j0 += EU) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
+                for (int u = 0; u < EU; ++u) {
                     rv[u] = rd[u] = rz[u] = P::zero();
                     rg[u] = 0.f;
                     if (j0 + u < here) {
                         rv[u] = P::ld(pv);
                         rd[u] = P::ld(pd);
-                        if (oz) {
+                        if (has_dz) {
                             rz[u] = P::ld(pz);
                             rg[u] = *pg;
                         }
                     }
                     pv += a.v.st;
                     pd += a.delta.st;
-                    if (oz) {
-                        pz += a.z.st;
-                        pg += g.dO.st;
-                    }
+                    pz += a.z.st;
+                    pg += g.dO.st;
                 }
+                const f32x2 bias2 = pack2(bias[m], bias[m]), skip2 = pack2(skip[m], skip[m]);
+                f32x2 dd2 = 0ull, db2 = 0ull;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int at = (j0 + u) * CH + cc;
-                    if (j0 + u < rows) {
-                        float dv = 0.f, ddl = 0.f, dz = 0.f;
-                        if (j0 + u < here) {
-                            const float gk = sDt[at], aw = sDv[at], dy = sDy[at];
-                            const float raw = Io<IO>::cvt(rd[u]) + bias[m], v = Io<IO>::cvt(rv[u]);
-                            const float dt = soft ? softplus(raw) : raw;
-                            dv = fmaf(dt, gk, skip[m] * dy);
-                            ddl = fmaf(v, gk, aw);
-                            if (soft) ddl *= sigmoid(raw);
-                            if (oz) dz = rg[u] * fmaf(skip[m], v, sY[at]) * silu_grad(Io<IO>::cvt(rz[u]));
-                            dd[m] = fmaf(dy, v, dd[m]);
-                            db[m] += ddl;
-                        }
-                        *ov = dv;
-                        *od = ddl;
-                        if (oz) *oz = dz;
+                for (int u = 0; u < EU; u += 2) {
+                    const float *at = sDt + (j0 + u) * CH + cc;   // the four arrays lie kChan apart
+                    auto both = [&](int which) { return pack2(at[which * Sh::kChan], at[which * Sh::kChan + CH]); };
+                    const f32x2 gk = both(0), aw = both(1), dy = both(2);
+                    const f32x2 v = pack2(Io<IO>::cvt(rv[u]), Io<IO>::cvt(rv[u + 1]));
+                    const f32x2 raw = add2(pack2(Io<IO>::cvt(rd[u]), Io<IO>::cvt(rd[u + 1])), bias2);
+                    f32x2 ddl = fma2(v, gk, aw), dt = raw;
+                    if (soft) {
+                        dt = softplus2(raw);
+                        ddl = mul2(ddl, sigmoid2(raw));
                     }
-                    ov += g.dv.st;
-                    od += g.ddelta.st;
-                    if (oz) oz += g.dz.st;
+                    const f32x2 dv = fma2(dt, gk, mul2(skip2, dy));
+                    float d0, d1, l0, l1, z0 = 0.f, z1 = 0.f;
+                    unpack2(dv, d0, d1);
+                    unpack2(ddl, l0, l1);
+                    if (has_dz) {
+                        const f32x2 z = pack2(Io<IO>::cvt(rz[u]), Io<IO>::cvt(rz[u + 1])), sg = sigmoid2(z);
+                        const f32x2 slope = mul2(sg, fma2(z, fma2(sg, pack2(-1.f, -1.f), pack2(1.f, 1.f)), pack2(1.f, 1.f)));
+                        unpack2(mul2(mul2(pack2(rg[u], rg[u + 1]), fma2(skip2, v, both(3))), slope), z0, z1);
+                    }
+                    const bool in0 = j0 + u < here, in1 = j0 + u + 1 < here;   // rows behind the end are 0
+                    l0 = in0 ? l0 : 0.f;
+                    l1 = in1 ? l1 : 0.f;
+                    dd2 = fma2(dy, v, dd2);     // dy is 0 there
+                    db2 = add2(db2, pack2(l0, l1));
+                    if (j0 + u < rows) {
+                        *ov = in0 ? d0 : 0.f;
+                        *od = l0;
+                        if (has_dz) *oz = in0 ? z0 : 0.f;
+                    }
+                    if (j0 + u + 1 < rows) {
+                        ov[g.dv.st] = in1 ? d1 : 0.f;
+                        od[g.ddelta.st] = l1;
+                        if (has_dz) oz[g.dz.st] = in1 ? z1 : 0.f;
+                    }
+                    ov += 2 * g.dv.st;
+                    od += 2 * g.ddelta.st;
+                    oz += 2 * g.dz.st;
                 }
+                dd[m] += sum2(dd2);
+                db[m] += sum2(db2);
             }
         }
         // ---- dq and dk: the warps' parts
