@@ -2,12 +2,13 @@
 // convolution p_t = bias + sum_{j<K} w_j x_{t-K+1+j}, y = act(p).
 //
 // Forward: 2 K flops for an element read once and written once, so the kernel is bound by HBM. A thread
-// owns V channels (16 bytes of them where pointers, strides and d allow it, else one channel) and walks
+// owns V channels (8 bytes of them where pointers, strides and d allow it, else one channel) and walks
 // a run of tokens with the last K - 1 inputs in registers. Neighbouring threads own neighbouring channels,
 // so every access of a warp is whole lines, whichever of token-major and head-major the two views are.
 // The inputs come ahead of their use through a ring in shared memory (kStages batches of kConvBatch tokens,
 // asynchronous copies into places that only the copying thread reads, so no barrier): bytes in flight cost no
-// registers. One channel a thread (V = 1): a batch's loads are in flight together. A run re-reads its K - 1
+// registers. Eight bytes a thread rather than 16 leave registers for four blocks an SM (B8 H16 T4096 d128 bf16: 59 us
+// against 72). One channel a thread (V = 1): a batch's loads are in flight together. A run re-reads its K - 1
 // first inputs (from L2).
 // Backward: the same walk with a second window, of dp: step t needs x_{t-K+1..t} for p_t and act', adds
 // dp_t x to dw, and emits dx_{t-K+1} = sum_j w_j dp_{t-j}. The walk goes K - 1 tokens past the run
@@ -82,7 +83,7 @@ template <int K, int V>
 __device__ __forceinline__ void load_weights(const falcon_conv_args_t &a, int h, int c0, float (&w)[K][V], float (&bias)[V]) {
     const float *p = a.w + ((long long)h * a.d + c0) * K;
     float f[K * V];   // (V channels, K taps) as they lie
-    if (V > 1 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {   // V K floats from c0 K: whole 16-byte words
+    if (V > 1 && V * K % 4 == 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {   // V K floats from c0 K: whole 16-byte words
 #pragma unroll
         for (int i = 0; i + 3 < K * V; i += 4) {
             const float4 x = *reinterpret_cast<const float4 *>(p + i);
@@ -123,7 +124,7 @@ __device__ __forceinline__ f32x2 taps(const f32x2 (&w)[K][N], const f32x2 (&past
 }
 
 template <typename IO, int K, int V, bool SILU>
-__global__ void __launch_bounds__(kConvThreads, K <= 5 ? 2 : 1) conv_fwd_kernel(falcon_conv_args_t a, ConvShape s) {
+__global__ void __launch_bounds__(kConvThreads, K <= 4 ? 4 : 2) conv_fwd_kernel(falcon_conv_args_t a, ConvShape s) {
     typedef Pack<IO, V> P;
     constexpr int kPast = Taps<K>::kPast, N = Pairs<V>::N;
     __shared__ __align__(16) typename P::raw ring[V > 1 ? kStages : 1][V > 1 ? kConvBatch : 1][V > 1 ? kConvThreads : 1];
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kConvThreads, K <= 5 ? 2 : 1) conv_fwd_kernel(
             if (V > 1) {
 #pragma unroll
                 for (int u = 0; u < kConvBatch; ++u) {
-                    if (ta + u < t1) copy_async<sizeof(typename P::raw) == 8 ? 8 : 16>(&ring[stage][u][me], ahead);
+                    if (ta + u < t1) copy_async<(int)sizeof(typename P::raw)>(&ring[stage][u][me], ahead);
                     ahead += a.x.st;
                 }
                 ta += kConvBatch;
@@ -249,7 +250,7 @@ struct True { static constexpr bool value = true; };
 struct False { static constexpr bool value = false; };
 
 template <typename IO, int K, int V, bool SILU>
-__global__ void __launch_bounds__(kConvThreads, K <= 4 ? 2 : 1) conv_bwd_kernel(falcon_conv_args_t a, falcon_conv_grads_t g, ConvShape s,
+__global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(falcon_conv_args_t a, falcon_conv_grads_t g, ConvShape s,
                                                                    float *part) {
     typedef Pack<IO, V> P;
     typedef Pack<float, V> F;
@@ -299,8 +300,8 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 2 : 1) conv_bwd_kernel(
 #pragma unroll
                 for (int u = 0; u < kConvBatch; ++u) {
                     if (ta + u < te) {
-                        copy_async<sizeof(typename P::raw) == 8 ? 8 : 16>(&ring_x[stage][u][me], ahead_x);
-                        copy_async<16>(&ring_g[stage][u][me], ahead_g);
+                        copy_async<(int)sizeof(typename P::raw)>(&ring_x[stage][u][me], ahead_x);
+                        copy_async<(int)sizeof(typename F::raw)>(&ring_g[stage][u][me], ahead_g);
                     }
                     ahead_x += a.x.st;
                     ahead_g += g.dy.st;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 2 : 1) conv_bwd_kernel(
 // Whether V channels go as one access: d and both the io and fp32 views.
 int conv_pack(const falcon_conv_args_t &a, const falcon_view_t *f32a, const falcon_view_t *f32b) {
     const int es = a.io_dtype == FALCON_BF16 ? 2 : 4;
-    const int V = f32a ? 4 : 16 / es;
+    const int V = f32a ? 2 : 8 / es;
     bool ok = a.d % V == 0 && view_packs(a.x, V, es);
     if (!f32a) ok = ok && view_packs(a.y, V, es);
     else ok = ok && view_packs(*f32a, V, 4) && view_packs(*f32b, V, 4);
@@ -535,7 +536,7 @@ cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &
 }
 
 ConvShape conv_bwd_shape(const falcon_conv_args_t &a, int V) {
-    return conv_shape(a, V, conv_run(a, V, 148 * 1024));
+    return conv_shape(a, V, conv_run(a, V, 148 * 512));
 }
 
 }  // namespace
@@ -545,21 +546,21 @@ cudaError_t launch_conv_fwd(const falcon_conv_args_t &a, int num_sms, cudaStream
     const int V = conv_pack(a, nullptr, nullptr);
     const ConvShape s = conv_shape(a, V, conv_run(a, V, (long long)num_sms * 2048));
     if (a.io_dtype == FALCON_BF16)
-        return V == 8 ? conv_fwd_io<__nv_bfloat16, 8>(a, s, st) : conv_fwd_io<__nv_bfloat16, 1>(a, s, st);
-    return V == 4 ? conv_fwd_io<float, 4>(a, s, st) : conv_fwd_io<float, 1>(a, s, st);
+        return V == 4 ? conv_fwd_io<__nv_bfloat16, 4>(a, s, st) : conv_fwd_io<__nv_bfloat16, 1>(a, s, st);
+    return V == 2 ? conv_fwd_io<float, 2>(a, s, st) : conv_fwd_io<float, 1>(a, s, st);
 }
 
 cudaError_t launch_conv_step(const falcon_conv_args_t &a, cudaStream_t st) {
     if ((long long)a.B * a.H == 0) return cudaSuccess;
     const int V = conv_pack(a, nullptr, nullptr);
-    if (a.io_dtype == FALCON_BF16) return V == 8 ? conv_step_io<__nv_bfloat16, 8>(a, st) : conv_step_io<__nv_bfloat16, 1>(a, st);
-    return V == 4 ? conv_step_io<float, 4>(a, st) : conv_step_io<float, 1>(a, st);
+    if (a.io_dtype == FALCON_BF16) return V == 4 ? conv_step_io<__nv_bfloat16, 4>(a, st) : conv_step_io<__nv_bfloat16, 1>(a, st);
+    return V == 2 ? conv_step_io<float, 2>(a, st) : conv_step_io<float, 1>(a, st);
 }
 
 // The workspace does not depend on the alignment of the views, so it is the larger of both packings'.
 size_t conv_bwd_workspace(const falcon_conv_args_t &a) {
     size_t most = 0;
-    for (int V = 1; V <= 4; V += 3) {
+    for (int V = 1; V <= 2; ++V) {
         const ConvShape s = conv_bwd_shape(a, V);
         const size_t bytes = (size_t)a.B * s.ntb * a.H * a.d * (a.K + 1) * sizeof(float);
         most = bytes > most ? bytes : most;
@@ -573,8 +574,8 @@ cudaError_t launch_conv_bwd(const falcon_conv_args_t &a, const falcon_conv_grads
     const ConvShape s = conv_bwd_shape(a, V);
     if (a.B > 0) {
         cudaError_t e;
-        if (a.io_dtype == FALCON_BF16) e = V == 4 ? conv_bwd_io<__nv_bfloat16, 4>(a, g, s, ws, st) : conv_bwd_io<__nv_bfloat16, 1>(a, g, s, ws, st);
-        else e = V == 4 ? conv_bwd_io<float, 4>(a, g, s, ws, st) : conv_bwd_io<float, 1>(a, g, s, ws, st);
+        if (a.io_dtype == FALCON_BF16) e = V == 2 ? conv_bwd_io<__nv_bfloat16, 2>(a, g, s, ws, st) : conv_bwd_io<__nv_bfloat16, 1>(a, g, s, ws, st);
+        else e = V == 2 ? conv_bwd_io<float, 2>(a, g, s, ws, st) : conv_bwd_io<float, 1>(a, g, s, ws, st);
         if (e != cudaSuccess) return e;
     }
     const long long HD = (long long)a.H * a.d, row = HD * (a.K + 1);   // dw (H,d,K), then dbias (H,d)

@@ -81,13 +81,13 @@ template <> struct Pack<__nv_bfloat16, 8> {
     }
 };
 
-// Asynchronous copy of 8 or 16 bytes into the thread's own place in shared memory, and the wait for all but the
+// Asynchronous copy of 4, 8 or 16 bytes into the thread's own place in shared memory, and the wait for all but the
 // newest N groups of them.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void *smem, const void *global) {
     const unsigned s = (unsigned)__cvta_generic_to_shared(smem);
     if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(global) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(global) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(global), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
