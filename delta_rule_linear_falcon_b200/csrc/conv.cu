@@ -33,16 +33,25 @@ struct ConvShape {
     long long ntb;   // blocks along the tokens
 };
 
-ConvShape conv_shape(const falcon_conv_args_t &a, int V, int run) {
+// Runs: so long that the blocks fill the `slots` that the SMs hold once, twice, .. (long runs re-read less of the past
+// and leave fewer partial rows; a part-filled last turn costs as much as a full one), and at most kLongest tokens.
+ConvShape conv_shape(const falcon_conv_args_t &a, int V, long long slots) {
+    constexpr long long kLongest = 160, kShortest = 8;
     ConvShape s;
     s.nv = (a.d + V - 1) / V;
     const long long packs = (long long)a.H * s.nv;
     s.bx = 32;
     while (s.bx < kConvThreads && s.bx < packs) s.bx *= 2;
     s.by = kConvThreads / s.bx;
-    s.run = run;
     s.ncb = (packs + s.bx - 1) / s.bx;
-    s.ntb = ((long long)a.T + (long long)run * s.by - 1) / ((long long)run * s.by);
+    long long run = kLongest;
+    for (int turns = 1; turns <= 8; ++turns) {
+        const long long rows = s.ncb * (a.B > 0 ? a.B : 1), tiles = slots * turns > rows ? slots * turns / rows : 1;
+        run = (a.T + tiles * s.by - 1) / (tiles * s.by);
+        if (run <= kLongest) break;
+    }
+    s.run = (int)(run > kLongest ? kLongest : run < kShortest ? kShortest : run);
+    s.ntb = ((long long)a.T + (long long)s.run * s.by - 1) / ((long long)s.run * s.by);
     if (s.ntb < 1) s.ntb = 1;
     return s;
 }
@@ -196,11 +205,11 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 4 : 2) conv_fwd_kernel(
                     for (int j = 0; j + 1 < K - 1; ++j) past[j][i] = past[j + 1][i];
                     if (K > 1) past[kPast - 1][i] = cur[i];
                 }
-                from_pairs<V>(p, out);
                 if (SILU) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) out[i] = silu(out[i]);
+                    for (int i = 0; i < N; ++i) p[i] = silu2(p[i]);
                 }
+                from_pairs<V>(p, out);
                 P::st(y, out);
                 y += a.y.st;
             }
@@ -327,21 +336,14 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(
             constexpr bool WHOLE = decltype(whole)::value;
             const bool live = WHOLE || t < n;
             f32x2 cur[N], d2[N], out[N];
-            float d[V];
             to_pairs<IO, V>(rx, cur);
-            F::cvt(rg, d);
-            if (SILU) {
-                f32x2 p2[N];
-                float p[V];
-#pragma unroll
-                for (int i = 0; i < N; ++i) p2[i] = taps<K, N>(w, past, cur[i], bias[i], i);
-                from_pairs<V>(p2, p);
-#pragma unroll
-                for (int i = 0; i < V; ++i) d[i] *= silu_grad(p[i]);
-            }
+            to_pairs<float, V>(rg, d2);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                d2[i] = pack2(d[2 * i], d[V > 1 ? 2 * i + 1 : 0]);
+                if (SILU) {   // silu'(p) = s (1 + p (1 - s)), s the sigmoid
+                    const f32x2 one = pack2(1.f, 1.f), p = taps<K, N>(w, past, cur[i], bias[i], i), sg = sigmoid2(p);
+                    d2[i] = mul2(d2[i], mul2(sg, fma2(p, fma2(sg, pack2(-1.f, -1.f), one), one)));
+                }
                 if (!live) d2[i] = 0ull;          // also where p or act'(p) is not finite
 #pragma unroll
                 for (int j = 0; j + 1 < K; ++j) dp[j][i] = dp[j + 1][i];
@@ -468,14 +470,6 @@ int conv_pack(const falcon_conv_args_t &a, const falcon_view_t *f32a, const falc
     return ok ? V : 1;
 }
 
-// Tokens of a thread's run: long runs re-read less of the past, short ones give more threads.
-int conv_run(const falcon_conv_args_t &a, int V, long long want_threads) {
-    const long long packs = (long long)a.H * ((a.d + V - 1) / V) * a.B;
-    int run = 128;
-    while (run > 8 && packs * ((a.T + run - 1) / run) < want_threads) run /= 2;
-    return run;
-}
-
 #define FALCON_CONV_TAPS(M)                                                            \
     switch (a.K) {                                                                     \
         case 1: M(1); break;                                                           \
@@ -536,7 +530,7 @@ cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &
 }
 
 ConvShape conv_bwd_shape(const falcon_conv_args_t &a, int V) {
-    return conv_shape(a, V, conv_run(a, V, 148 * 512));
+    return conv_shape(a, V, 148 * (a.K <= 4 ? 3 : 2));
 }
 
 }  // namespace
@@ -544,7 +538,7 @@ ConvShape conv_bwd_shape(const falcon_conv_args_t &a, int V) {
 cudaError_t launch_conv_fwd(const falcon_conv_args_t &a, int num_sms, cudaStream_t st) {
     if ((long long)a.B * a.H == 0) return cudaSuccess;
     const int V = conv_pack(a, nullptr, nullptr);
-    const ConvShape s = conv_shape(a, V, conv_run(a, V, (long long)num_sms * 2048));
+    const ConvShape s = conv_shape(a, V, (long long)num_sms * (a.K <= 4 ? 4 : 2));
     if (a.io_dtype == FALCON_BF16)
         return V == 4 ? conv_fwd_io<__nv_bfloat16, 4>(a, s, st) : conv_fwd_io<__nv_bfloat16, 1>(a, s, st);
     return V == 2 ? conv_fwd_io<float, 2>(a, s, st) : conv_fwd_io<float, 1>(a, s, st);
