@@ -520,8 +520,10 @@ cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &
 #define FALCON_RUN(K)                                                                             \
     {                                                                                             \
         const auto kern = a.act == FALCON_ACT_SILU ? conv_bwd_kernel<IO, K, V, true> : conv_bwd_kernel<IO, K, V, false>; \
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
-        if (e != cudaSuccess) return e;                                                           \
+        if (smem > 48 * 1024) {                                                                   \
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
+            if (e != cudaSuccess) return e;                                                       \
+        }                                                                                         \
         kern<<<(unsigned)blocks, block, smem, st>>>(a, g, s, ws);                                 \
     }
     FALCON_CONV_TAPS(FALCON_RUN)

@@ -431,6 +431,20 @@ def _call(name, *args):
         raise FalconError(st, name)
 
 
+def _dense(shape, dtype, dev):
+    """An uninitialised contiguous tensor."""
+    s, strides = 1, []
+    for n in reversed(shape):
+        strides.append(s)
+        s *= n if n > 1 else 1
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=dev)
+
+
+def _token_major(B, H, T, d, dev):
+    """An uninitialised fp32 (B, H, T, d) view of token-major rows."""
+    return torch.empty_strided((B, H, T, d), (T * H * d, d, H * d, 1), dtype=torch.float32, device=dev)
+
+
 def _workspace(workspace, need, dev):
     """(tensor, address, bytes) of the caller's workspace or of one made here."""
     if workspace is None:
@@ -467,9 +481,9 @@ def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=
     ctx, raw = _on(x.device, stream)
     with ctx:
         if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            y = _dense(shape, x.dtype, x.device)
         if state_out is None and want_state:
-            state_out = torch.empty(tail, dtype=x.dtype, device=x.device)
+            state_out = _dense(tail, x.dtype, x.device)
         a = _conv_args(x, w, bias, act, state, lengths, shape, tail, y, state_out)
         _call("falcon_conv_fwd", ctypes.byref(a), raw)
     return y, state_out
@@ -484,7 +498,7 @@ def falcon_conv_step(x, w, state, *, bias=None, act="silu", state_out=None, y=No
     ctx, raw = _on(x.device, stream)
     with ctx:
         if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            y = _dense(shape, x.dtype, x.device)
         a = _conv_args(x, w, bias, act, state, None, shape, (N, H, max(w.shape[2] - 1, 0), d), y,
                        state if state_out is None else state_out)
         _call("falcon_conv_step", ctypes.byref(a), raw)
@@ -505,10 +519,10 @@ def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None
     ctx, raw = _on(dev, stream)
     with ctx:
         if dx is None:
-            dx = torch.empty((B, T, H, d), dtype=f32, device=dev).transpose(1, 2)
-        out = {"dx": dx, "dw": torch.empty((H, d, K), dtype=f32, device=dev),
-               "dbias": torch.empty((H, d), dtype=f32, device=dev) if bias is not None else None,
-               "dstate": torch.empty(tail, dtype=f32, device=dev) if state is not None else None}
+            dx = _token_major(B, H, T, d, dev)
+        out = {"dx": dx, "dw": _dense((H, d, K), f32, dev),
+               "dbias": _dense((H, d), f32, dev) if bias is not None else None,
+               "dstate": _dense(tail, f32, dev) if state is not None else None}
         a = _conv_args(x, w, bias, act, state, lengths, shape, tail, None, None)
         g = FalconConvGrads(_seq(dy, "dy", shape, f32, dev), _arr(dstate_out, "dstate_out", tail, f32, dev),
                             _seq(dx, "dx", shape, f32, dev), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"]))
@@ -554,9 +568,9 @@ def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softp
     ctx, raw = _on(dev, stream)
     with ctx:
         if o is None:
-            o = torch.empty(vs, dtype=v.dtype, device=dev)
+            o = _dense(vs, v.dtype, dev)
         if S_out is None and want_state:
-            S_out = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+            S_out = _dense((B, H, dv, dk), torch.float32, dev)
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, o, S_out)
         workspace, p, n = _workspace(workspace, falcon_scan_workspace_size(a) if workspace is None else 0, dev)
         _call("falcon_scan_fwd", ctypes.byref(a), p, n, raw)
@@ -571,7 +585,7 @@ def falcon_scan_step(q, k, v, delta, A, S, *, D=None, z=None, delta_bias=None, s
     ctx, raw = _on(v.device, stream)
     with ctx:
         if o is None:
-            o = torch.empty(vs, dtype=v.dtype, device=v.device)
+            o = _dense(vs, v.dtype, v.device)
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, None, S, o, S if S_out is None else S_out)
         _call("falcon_scan_step", ctypes.byref(a), raw)
     return o
@@ -587,13 +601,13 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
     dev, f32 = v.device, torch.float32
     ctx, raw = _on(dev, stream)
     with ctx:
-        rows = lambda d: torch.empty((B, T, H, d), dtype=f32, device=dev).transpose(1, 2)
+        rows = lambda d: _token_major(B, H, T, d, dev)
         out = {"dq": rows(dk), "dk": rows(dk), "dv": rows(dv), "ddelta": rows(dv),
                "dz": rows(dv) if z is not None else None,
-               "dA": torch.empty((H, dv, dk), dtype=f32, device=dev),
-               "dD": torch.empty((H, dv), dtype=f32, device=dev) if D is not None else None,
-               "ddelta_bias": torch.empty((H, dv), dtype=f32, device=dev) if delta_bias is not None else None,
-               "dS0": torch.empty((B, H, dv, dk), dtype=f32, device=dev) if S0 is not None else None}
+               "dA": _dense((H, dv, dk), f32, dev),
+               "dD": _dense((H, dv), f32, dev) if D is not None else None,
+               "ddelta_bias": _dense((H, dv), f32, dev) if delta_bias is not None else None,
+               "dS0": _dense((B, H, dv, dk), f32, dev) if S0 is not None else None}
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, None, None)
         g = FalconScanGrads(_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev),
                             *(_seq(out[n], n, s, f32, dev) for n, s in (("dq", ks), ("dk", ks), ("dv", vs), ("ddelta", vs), ("dz", vs))),
@@ -636,9 +650,9 @@ def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, la
     ctx, raw = _on(x.device, stream)
     with ctx:
         if q_out is None and q is not None:
-            q_out = torch.empty(qs, dtype=x.dtype, device=x.device)
+            q_out = _dense(qs, x.dtype, x.device)
         if k_out is None and k is not None:
-            k_out = torch.empty(ks, dtype=x.dtype, device=x.device)
+            k_out = _dense(ks, x.dtype, x.device)
         a = _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
         _call("falcon_qknorm_fwd", ctypes.byref(a), raw)
     return q_out, k_out
@@ -653,10 +667,10 @@ def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps
     dev, f32 = x.device, torch.float32
     ctx, raw = _on(dev, stream)
     with ctx:
-        rows = lambda s: torch.empty((s[0], s[2], s[1], s[3]), dtype=f32, device=dev).transpose(1, 2)
+        rows = lambda s: _token_major(*s, dev)
         out = {"dq": rows(qs) if q is not None else None, "dk": rows(ks) if k is not None else None,
-               "dwq": torch.empty(qs[3:], dtype=f32, device=dev) if wq is not None else None,
-               "dwk": torch.empty(qs[3:], dtype=f32, device=dev) if wk is not None else None}
+               "dwq": _dense(qs[3:], f32, dev) if wq is not None else None,
+               "dwk": _dense(qs[3:], f32, dev) if wk is not None else None}
         a = _qknorm_args(x, qs, ks, q, k, None, None, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
         g = FalconQknormGrads(_seq(dq_out, "dq_out", qs, f32, dev), _seq(dk_out, "dk_out", ks, f32, dev),
                               _seq(out["dq"], "dq", qs, f32, dev), _seq(out["dk"], "dk", ks, f32, dev),
