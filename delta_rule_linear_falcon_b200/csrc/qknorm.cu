@@ -81,12 +81,6 @@ __device__ __forceinline__ float lanes_total(float x) {
     return x;
 }
 
-// Backward: rows in flight in the ring (few enough for two blocks an SM), and the bytes before it.
-__host__ __device__ constexpr int norm_ring(int V, int NV) { return V == 1 ? 1 : NV > 1 ? 3 : 5; }
-__host__ __device__ inline size_t norm_turn_bytes(const falcon_qknorm_args_t &a, int V, int tokens) {
-    return ((size_t)tokens * turn_slots(a, V) * sizeof(float2) + 15) / 16 * 16;
-}
-
 // A pack of a row in registers: the first channels of its pairs, then the second ones. `row` points at the row's
 // first channel.
 template <typename E, int V, bool HALF> struct Row {
@@ -106,10 +100,6 @@ template <typename E, int V, bool HALF> struct Row {
     };
     static __device__ __forceinline__ raw zero() { return raw{P::zero(), P::zero()}; }
     static __device__ __forceinline__ raw ld(const E *row, Place at) { return raw{P::ld(row + at.a), P::ld(row + at.b)}; }
-    static __device__ __forceinline__ void ask(raw *to, const E *row, Place at) {
-        copy_async<sizeof(typename P::raw)>(&to->a, row + at.a);
-        copy_async<sizeof(typename P::raw)>(&to->b, row + at.b);
-    }
     static __device__ __forceinline__ void cvt(const raw &r, float (&x)[V]) {
         float u[H], v[H];
         P::cvt(r.a, u);
@@ -142,7 +132,6 @@ template <typename E, bool HALF> struct Row<E, 1, HALF> {
     static __device__ __forceinline__ int channel(int p, int, int) { return p; }
     static __device__ __forceinline__ raw zero() { return P::zero(); }
     static __device__ __forceinline__ raw ld(const E *row, Place at) { return P::ld(row + at.a); }
-    static __device__ __forceinline__ void ask(raw *, const E *, Place) {}
     static __device__ __forceinline__ void cvt(raw r, float (&x)[1]) { P::cvt(r, x); }
     static __device__ __forceinline__ void st(E *row, Place at, const float (&x)[1]) { P::st(row + at.a, x); }
 };
@@ -330,13 +319,8 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
     typedef Row<IO, V, HALF> R;
     typedef Row<float, V, HALF> F;
     constexpr int G = kNormThreads / LANES;
-    constexpr int RING = norm_ring(V, NV);          // rows in flight
-    extern __shared__ __align__(16) char smem[];    // the rotation's factors, then the ring
-    float2 *cs = reinterpret_cast<float2 *>(smem);
-    typedef typename R::raw RingX[NV][kNormThreads];
-    typedef typename F::raw RingU[NV][kNormThreads];
-    RingU *ring_u = reinterpret_cast<RingU *>(smem + norm_turn_bytes(a, V, G));
-    RingX *ring_x = reinterpret_cast<RingX *>(ring_u + RING);
+    constexpr int kRows = V == 1 || NV > 1 ? 1 : 2;   // rows worked on together, as many more on their way
+    extern __shared__ __align__(16) float2 cs[];
     __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
     __shared__ float sw[2][kMaxWidth];
     float *stage = stage_all[V == 1 ? threadIdx.x >> 5 : 0];
@@ -363,32 +347,6 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
         const int b = there ? (int)(tok / a.T) : 0, t = there ? (int)(tok - (long long)b * a.T) : 0;
         const bool live = there && t < seq_length(a.lengths, b, a.T);
 
-        // the rows of the walk, queries and then keys, asked for ahead of their use
-        int ha = h0;
-        const IO *ahead_x = ha < a.Hq ? row_of<IO>(a.q, b, ha, t) : row_of<IO>(a.k, b, ha - a.Hq, t);
-        const float *ahead_u = ha < a.Hq ? row_of<float>(g.dq_out, b, ha, t) : row_of<float>(g.dk_out, b, ha - a.Hq, t);
-        auto ask = [&](int place) {
-            if (V == 1) return;
-            if (live && ha < h1) {
-#pragma unroll
-                for (int m = 0; m < NV; ++m)
-                    if ((lane + m * LANES) * V < a.d) {
-                        R::ask(&ring_x[place][m][threadIdx.x], ahead_x, typename R::Place(lane + m * LANES, a.rot));
-                        F::ask(&ring_u[place][m][threadIdx.x], ahead_u, typename F::Place(lane + m * LANES, a.rot));
-                    }
-            }
-            ++ha;
-            ahead_x += ha > a.Hq ? a.k.sh : a.q.sh;
-            ahead_u += ha > a.Hq ? g.dk_out.sh : g.dq_out.sh;
-            if (ha == a.Hq && a.Hk > 0) {
-                ahead_x = row_of<IO>(a.k, b, 0, t);
-                ahead_u = row_of<float>(g.dk_out, b, 0, t);
-            }
-            copy_commit();
-        };
-#pragma unroll
-        for (int i = 0; i < RING - 1; ++i) ask(i);
-
         Turn<V, LANES, NV, HALF> turn;
         if (a.rot > 0) {
             __syncthreads();
@@ -396,7 +354,6 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
             __syncthreads();
             turn.load(a, lane, cs + slot * turn_slots(a, V), -1.f);
         }
-        int place = 0, free_place = RING - 1;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const falcon_view_t &in = which ? a.k : a.q, &up = which ? g.dk_out : g.dq_out, &to = which ? g.dk : g.dq;
@@ -411,107 +368,127 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
                     const int p = lane + m * LANES;
                     w[m][i] = weight && p * V < a.d ? weight[R::channel(p, i, a.rot)] : 1.f;
                 }
+            const IO *px = row_of<IO>(in, b, first, t);
+            const float *pu = row_of<float>(up, b, first, t);
             float *po = row_of<float>(to, b, first, t);
-            for (int h = first; h < last; ++h) {
-                float x[NV][V], u[NV][V];
-                if (V > 1) {
-                    ask(free_place);
-                    free_place = free_place + 1 < RING ? free_place + 1 : 0;
-                    copy_wait<RING - 1>();
-                }
+            typename R::raw rx[kRows][NV];
+            typename F::raw ru[kRows][NV];
+            auto fetch = [&](int h) {
 #pragma unroll
-                for (int m = 0; m < NV; ++m) {
-                    const int p = lane + m * LANES;
-                    const bool mine = live && p * V < a.d;
-                    typename R::raw rx = R::zero();
-                    typename F::raw ru = F::zero();
-                    if (mine) {
-                        rx = V > 1 ? ring_x[place][m][threadIdx.x] : R::ld(row_of<IO>(in, b, h, t), typename R::Place(p, a.rot));
-                        ru = V > 1 ? ring_u[place][m][threadIdx.x] : F::ld(row_of<float>(up, b, h, t), typename F::Place(p, a.rot));
-                    }
-                    R::cvt(rx, x[m]);
-                    F::cvt(ru, u[m]);
-                }
-                if (V > 1) place = place + 1 < RING ? place + 1 : 0;
-                if constexpr (V > 1) {   // two channels an instruction
-                    constexpr int H = V / 2, Q = V / 4;
-                    f32x2 x1[NV][Q], x2[NV][Q], u1[NV][Q], u2[NV][Q], sum = 0ull;
-#pragma unroll
-                    for (int m = 0; m < NV; ++m)
-#pragma unroll
-                        for (int i = 0; i < Q; ++i) {
-                            x1[m][i] = pack2(x[m][2 * i], x[m][2 * i + 1]);
-                            x2[m][i] = pack2(x[m][H + 2 * i], x[m][H + 2 * i + 1]);
-                            sum = fma2(x1[m][i], x1[m][i], sum);
-                            sum = fma2(x2[m][i], x2[m][i], sum);
-                        }
-                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(sum2(sum)), scale);
-                    const f32x2 ri2 = pack2(ri, ri);
-                    sum = 0ull;
-#pragma unroll
-                    for (int m = 0; m < NV; ++m)
-#pragma unroll
-                        for (int i = 0; i < Q; ++i) {
-                            u1[m][i] = pack2(u[m][2 * i], u[m][2 * i + 1]);
-                            u2[m][i] = pack2(u[m][H + 2 * i], u[m][H + 2 * i + 1]);
-                            if (a.rot > 0) {
-                                const f32x2 c = pack2(turn.c[m][2 * i], turn.c[m][2 * i + 1]);
-                                const f32x2 sn = pack2(turn.s[m][2 * i], turn.s[m][2 * i + 1]);
-                                const f32x2 ns = pack2(-turn.s[m][2 * i], -turn.s[m][2 * i + 1]);
-                                const f32x2 y = fma2(u1[m][i], c, mul2(u2[m][i], ns));
-                                u2[m][i] = fma2(u2[m][i], c, mul2(u1[m][i], sn));
-                                u1[m][i] = y;
-                            }
-                            x1[m][i] = mul2(x1[m][i], ri2);
-                            x2[m][i] = mul2(x2[m][i], ri2);
-                            if (part) {      // rows that are not there are zero
-                                dw2[which][m][i] = fma2(u1[m][i], x1[m][i], dw2[which][m][i]);
-                                dw2[which][m][Q + i] = fma2(u2[m][i], x2[m][i], dw2[which][m][Q + i]);
-                            }
-                            u1[m][i] = mul2(u1[m][i], pack2(w[m][2 * i], w[m][2 * i + 1]));
-                            u2[m][i] = mul2(u2[m][i], pack2(w[m][H + 2 * i], w[m][H + 2 * i + 1]));
-                            sum = fma2(u1[m][i], x1[m][i], sum);
-                            sum = fma2(u2[m][i], x2[m][i], sum);
-                        }
-                    const float dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(sum2(sum)) * scale;
-                    const f32x2 dot2 = pack2(dot, dot);
-#pragma unroll
-                    for (int m = 0; m < NV; ++m)
-#pragma unroll
-                        for (int i = 0; i < Q; ++i) {
-                            unpack2(mul2(ri2, fma2(x1[m][i], dot2, u1[m][i])), u[m][2 * i], u[m][2 * i + 1]);
-                            unpack2(mul2(ri2, fma2(x2[m][i], dot2, u2[m][i])), u[m][H + 2 * i], u[m][H + 2 * i + 1]);
-                        }
-                } else {
-                    float ss = 0.f, dot = 0.f;
-#pragma unroll
-                    for (int m = 0; m < NV; ++m) ss = fmaf(x[m][0], x[m][0], ss);
-                    const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss), scale);
-                    if (a.rot > 0) turn.apply(u, lane, stage);
+                for (int r = 0; r < kRows; ++r) {
 #pragma unroll
                     for (int m = 0; m < NV; ++m) {
-                        x[m][0] *= ri;
-                        dw[which][m] = fmaf(u[m][0], x[m][0], dw[which][m]);
-                        u[m][0] *= w[m][0];
-                        dot = fmaf(u[m][0], x[m][0], dot);
+                        const int p = lane + m * LANES;
+                        rx[r][m] = R::zero();
+                        ru[r][m] = F::zero();
+                        if (live && h + r < last && p * V < a.d) {
+                            rx[r][m] = R::ld(px, typename R::Place(p, a.rot));
+                            ru[r][m] = F::ld(pu, typename F::Place(p, a.rot));
+                        }
                     }
-                    dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(dot) * scale;
-#pragma unroll
-                    for (int m = 0; m < NV; ++m) u[m][0] = ri * fmaf(x[m][0], dot, u[m][0]);
+                    px += in.sh;
+                    pu += up.sh;
                 }
-                if (there) {
+            };
+            fetch(first);
+            for (int h = first; h < last; h += kRows) {
+                typename R::raw cx[kRows][NV];
+                typename F::raw cu[kRows][NV];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
 #pragma unroll
                     for (int m = 0; m < NV; ++m) {
-                        if (!live)
-#pragma unroll
-                            for (int i = 0; i < V; ++i) u[m][i] = 0.f;
-                        if ((lane + m * LANES) * V < a.d) F::st(po, typename F::Place(lane + m * LANES, a.rot), u[m]);
+                        cx[r][m] = rx[r][m];
+                        cu[r][m] = ru[r][m];
                     }
+                if (h + kRows < last) fetch(h + kRows);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float x[NV][V], u[NV][V];
+#pragma unroll
+                    for (int m = 0; m < NV; ++m) {
+                        R::cvt(cx[r][m], x[m]);
+                        F::cvt(cu[r][m], u[m]);
+                    }
+                    if constexpr (V > 1) {   // two channels an instruction
+                        constexpr int H = V / 2, Q = V / 4;
+                        f32x2 x1[NV][Q], x2[NV][Q], u1[NV][Q], u2[NV][Q], sum = 0ull;
+#pragma unroll
+                        for (int m = 0; m < NV; ++m)
+#pragma unroll
+                            for (int i = 0; i < Q; ++i) {
+                                x1[m][i] = pack2(x[m][2 * i], x[m][2 * i + 1]);
+                                x2[m][i] = pack2(x[m][H + 2 * i], x[m][H + 2 * i + 1]);
+                                sum = fma2(x1[m][i], x1[m][i], sum);
+                                sum = fma2(x2[m][i], x2[m][i], sum);
+                            }
+                        const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(sum2(sum)), scale);
+                        const f32x2 ri2 = pack2(ri, ri);
+                        sum = 0ull;
+#pragma unroll
+                        for (int m = 0; m < NV; ++m)
+#pragma unroll
+                            for (int i = 0; i < Q; ++i) {
+                                u1[m][i] = pack2(u[m][2 * i], u[m][2 * i + 1]);
+                                u2[m][i] = pack2(u[m][H + 2 * i], u[m][H + 2 * i + 1]);
+                                if (a.rot > 0) {
+                                    const f32x2 c = pack2(turn.c[m][2 * i], turn.c[m][2 * i + 1]);
+                                    const f32x2 sn = pack2(turn.s[m][2 * i], turn.s[m][2 * i + 1]);
+                                    const f32x2 ns = pack2(-turn.s[m][2 * i], -turn.s[m][2 * i + 1]);
+                                    const f32x2 y = fma2(u1[m][i], c, mul2(u2[m][i], ns));
+                                    u2[m][i] = fma2(u2[m][i], c, mul2(u1[m][i], sn));
+                                    u1[m][i] = y;
+                                }
+                                x1[m][i] = mul2(x1[m][i], ri2);
+                                x2[m][i] = mul2(x2[m][i], ri2);
+                                if (part) {      // rows that are not there are zero
+                                    dw2[which][m][i] = fma2(u1[m][i], x1[m][i], dw2[which][m][i]);
+                                    dw2[which][m][Q + i] = fma2(u2[m][i], x2[m][i], dw2[which][m][Q + i]);
+                                }
+                                u1[m][i] = mul2(u1[m][i], pack2(w[m][2 * i], w[m][2 * i + 1]));
+                                u2[m][i] = mul2(u2[m][i], pack2(w[m][H + 2 * i], w[m][H + 2 * i + 1]));
+                                sum = fma2(u1[m][i], x1[m][i], sum);
+                                sum = fma2(u2[m][i], x2[m][i], sum);
+                            }
+                        const float dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(sum2(sum)) * scale;
+                        const f32x2 dot2 = pack2(dot, dot);
+#pragma unroll
+                        for (int m = 0; m < NV; ++m)
+#pragma unroll
+                            for (int i = 0; i < Q; ++i) {
+                                unpack2(mul2(ri2, fma2(x1[m][i], dot2, u1[m][i])), u[m][2 * i], u[m][2 * i + 1]);
+                                unpack2(mul2(ri2, fma2(x2[m][i], dot2, u2[m][i])), u[m][H + 2 * i], u[m][H + 2 * i + 1]);
+                            }
+                    } else {
+                        float ss = 0.f, dot = 0.f;
+#pragma unroll
+                        for (int m = 0; m < NV; ++m) ss = fmaf(x[m][0], x[m][0], ss);
+                        const float ri = root_inverse(a, a.norm == FALCON_NORM_NONE ? 0.f : lanes_total<LANES>(ss), scale);
+                        if (a.rot > 0) turn.apply(u, lane, stage);
+#pragma unroll
+                        for (int m = 0; m < NV; ++m) {
+                            x[m][0] *= ri;
+                            dw[which][m] = fmaf(u[m][0], x[m][0], dw[which][m]);
+                            u[m][0] *= w[m][0];
+                            dot = fmaf(u[m][0], x[m][0], dot);
+                        }
+                        dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(dot) * scale;
+#pragma unroll
+                        for (int m = 0; m < NV; ++m) u[m][0] = ri * fmaf(x[m][0], dot, u[m][0]);
+                    }
+                    if (there && h + r < last) {
+#pragma unroll
+                        for (int m = 0; m < NV; ++m) {
+                            if (!live)
+#pragma unroll
+                                for (int i = 0; i < V; ++i) u[m][i] = 0.f;
+                            if ((lane + m * LANES) * V < a.d) F::st(po, typename F::Place(lane + m * LANES, a.rot), u[m]);
+                        }
+                    }
+                    po += to.sh;
                 }
-                po += to.sh;
             }
         }
-        copy_wait<0>();
     }
     if (!part) return;
     // the block's sums, lane group by lane group in order
@@ -579,12 +556,8 @@ NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
 template <typename IO, int V, int LANES, int NV, bool HALF>
 cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
     const NormShape s = norm_shape(a, LANES);
-    size_t smem = norm_turn_bytes(a, V, kNormThreads / LANES);
+    const size_t smem = (size_t)(kNormThreads / LANES) * turn_slots(a, V) * sizeof(float2);
     if (g) {
-        if (V > 1) smem += (size_t)norm_ring(V, NV) * NV * kNormThreads * V * (sizeof(IO) + sizeof(float));
-        const cudaError_t e = cudaFuncSetAttribute(qknorm_bwd_kernel<IO, V, LANES, NV, HALF>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
         qknorm_bwd_kernel<IO, V, LANES, NV, HALF><<<s.blocks, kNormThreads, smem, st>>>(a, *g, s, part);
     } else {
         if (s.groups > kMaxGrid || s.parts > 65535) return cudaErrorInvalidConfiguration;
