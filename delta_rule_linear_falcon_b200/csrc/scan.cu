@@ -10,7 +10,8 @@
 // because it competes with those exponentials for the instruction slots: v, delta and z of kScanChunk tokens come
 // as 16-byte asynchronous copies into a ring in shared memory, one copy a thread and tensor, and are read there at
 // fixed offsets; o goes back the same way, in the place of z (or v) (loads and stores of single elements, with
-// their addresses, took a fifth of the pass). Where rows are not 16-byte multiples, elements are copied one by one.
+// their addresses, took a fifth of the pass). Where rows are not 16-byte multiples, elements are copied one by one
+// (B1 T16384 dv2048 off alignment: 511 us against 370).
 // q_t and k_t, the same for all channels of a head, are staged in fp32 and read as broadcasts. Step sizes (softplus)
 // are computed two tokens an instruction, once per channel and token.
 //
@@ -18,6 +19,9 @@
 // cut into segments (scan_plan). A first launch runs every segment from a zero state and leaves its end
 // state E and the sum of its steps sd, from which the decay over the segment is exp(A sd); in the second
 // each segment joins the states before it, S <- exp(A sd_j) S + E_j, and runs with outputs.
+// Measured, bf16, dk = 16: B4 H16 T2048 dv128 (64 blocks unsplit) 196 us in 9 segments, 398 us unsplit; the
+// exponential unit is at 81% in the first launch and 72% in the second. B1 T16384 dv2048: 370 us in 37 segments. 512
+// blocks unsplit (B32 H16 T1024 dv128): 458 us, 115 us for each 2^28 entries, whose exponentials alone are 58 us.
 #include "scan.cuh"
 
 namespace falcon {
@@ -366,7 +370,8 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
 // One token. A channel's row of the state is read and written by G lanes, four columns each, so the state
 // moves in whole lines; each thread has the rows of kStepRows channels in flight, and those of the next sequence
 // while it works on this one's. A block takes the same channels of several sequences: A, as large as a sequence's
-// state, is read once for them. A channel's scalars (step, dt v, output) belong to one of its lanes.
+// state, is read once for them (256 sequences, H32 dv128 dk16: 35 us for each launch alone with eight, 41 with one; 4.9
+// TB/s among others). A channel's scalars (step, dt v, output) belong to one of its lanes.
 constexpr int kStepThreads = 128, kStepRows = 4;
 
 template <typename IO, int G, bool V4>

@@ -16,6 +16,10 @@
 // Step 3 sums over channels (dq, dk) and over columns (dv, ddelta, dz) of the same products. A thread owns
 // 4 channels x 4 columns, SL = dk / 4 lanes side by side: the first additions of either sum are fused
 // multiply-adds in registers, the rest 3 to 6 shuffles (lanes_sum) for 16 entries.
+// B2 H16 T2048 dv128 dk16, bf16: 82 us for step 1, 30 for the joins, 255 for step 3, 17 for the sums. Step 3 is bound by
+// latency at 12 warps an SM (168 registers, half of them states; 70 KB of shared memory): its instruction slots are at
+// half, the exponential unit at 40%. Taken out one at a time, the channels' gradients at a segment's end were 55 us of it
+// (45 since they are formed two tokens an instruction), the shuffled sums 28, the exponentials 19.
 #include "scan.cuh"
 
 namespace falcon {
@@ -543,7 +547,8 @@ struct BwdSizes {
 };
 
 // Segments of a walk: as many as leave four blocks of step 3 for each place on an SM. Long walks make few joins, and
-// few parts of dA (each as large as the state).
+// few parts of dA (each as large as the state): 437 us in all with one segment for the case above, 385 with two, 382
+// with four, 470 with eight, whose blocks no longer fill the SMs.
 BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     BwdSizes z;
     z.nseg = (a.T + kSeg - 1) / kSeg;

@@ -325,6 +325,9 @@ FALCON_API falcon_status_t falcon_decode_step(int rule, int io_dtype, int N, int
  *    they were, rows of gradients there are written 0, and final states are those after the last
  *    token of the sequence.
  *  - Sums over tokens are taken in a fixed order: repeated calls give the same bits.
+ *  - A workspace is used only while the call's kernels run on `stream`; calls that can overlap on the GPU (other
+ *    streams, graphs replayed side by side) need workspaces of their own. The first call of the library on a device
+ *    looks up its properties: make it before any stream capture.
  * ------------------------------------------------------------------------------------------ */
 typedef struct {
     void *p;              /* device memory, or NULL where the tensor is optional */
@@ -395,9 +398,9 @@ FALCON_API falcon_status_t falcon_conv_bwd(const falcon_conv_args_t *args, const
  *   o_t[i]    = (sum_c S_t[i,c] q_t[c] + D[i] v_t[i]) silu(z_t[i])
  * (the terms of D, delta_bias and z only where those are given). dt A <= 0 is a precondition: the
  * decays lie in [0, 1]; it is not checked per element. The state, the decays and all sums are fp32.
- * Supported: 1 <= dk <= 128; any dv >= 1; fp32 or bf16.
- * Workspace: with few channels the sequence is split into segments that run at once, in three
- * steps (each segment from a zero state, the states between them, each segment from its state).
+ * Supported: 1 <= dk <= 128; any dv >= 1; token strides up to 2^28 elements; fp32 or bf16.
+ * Workspace: with few channels the sequence is split into segments that run at once, in two
+ * launches (each segment from a zero state; then each from the joined states before it).
  * falcon_scan_workspace_size(args) bytes, 16-byte aligned, are needed for that, 0 where it does not
  * pay; with less, or NULL, the sequence is not split. Results differ by rounding only.
  * S_out may be the same memory as S0. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
