@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -114,6 +115,11 @@ class FalconQknormGrads(ctypes.Structure):
     _fields_ = [("dq_out", FalconView), ("dk_out", FalconView), ("dq", FalconView), ("dk", FalconView),
                 ("dwq", _P), ("dwk", _P)]
 
+# The same structs as bytes, for the calls below: packing takes a quarter of the time of filling a ctypes.Structure.
+_VIEW = "Pqqq"
+_CONV_ARGS, _CONV_GRADS = struct.Struct("@7i" + 2 * _VIEW + "5P"), struct.Struct("@" + _VIEW + "P" + _VIEW + "3P")
+_SCAN_ARGS, _SCAN_GRADS = struct.Struct("@7i" + 6 * _VIEW + "6P"), struct.Struct("@" + _VIEW + "P" + 5 * _VIEW + "4P")
+_QKNORM_ARGS, _QKNORM_GRADS = struct.Struct("@9i" + 4 * _VIEW + "2Pf3P"), struct.Struct("@" + 4 * _VIEW + "2P")
 
 _lib = None
 _lock = threading.Lock()
@@ -142,9 +148,8 @@ def lib() -> ctypes.CDLL:
             L.falcon_bwd_recurrent.restype = i
             L.falcon_decode_step.argtypes = [i, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, f, vp, vp]
             L.falcon_decode_step.restype = i
-            for name, args, grads in (("conv", FalconConvArgs, FalconConvGrads), ("scan", FalconScanArgs, FalconScanGrads),
-                                      ("qknorm", FalconQknormArgs, FalconQknormGrads)):
-                A, G = ctypes.POINTER(args), ctypes.POINTER(grads)
+            for name in ("conv", "scan", "qknorm"):
+                A = G = vp   # the address of a struct, or its packed bytes
                 fwd, bwd = getattr(L, f"falcon_{name}_fwd"), getattr(L, f"falcon_{name}_bwd")
                 fwd.argtypes = [A, vp, ctypes.c_size_t, vp] if name == "scan" else [A, vp]
                 bwd.argtypes = [A, G, vp, ctypes.c_size_t, vp]
@@ -154,7 +159,7 @@ def lib() -> ctypes.CDLL:
                 if name != "qknorm":
                     step = getattr(L, f"falcon_{name}_step")
                     step.argtypes, step.restype = [A, vp], i
-            L.falcon_scan_workspace_size.argtypes = [ctypes.POINTER(FalconScanArgs)]
+            L.falcon_scan_workspace_size.argtypes = [vp]
             L.falcon_scan_workspace_size.restype = ctypes.c_size_t
             L.falcon_status_string.argtypes = [i]
             L.falcon_status_string.restype = ctypes.c_char_p
@@ -361,7 +366,7 @@ def falcon_decode_step(S, k_prev, q, k, v, alpha, eta, *, rule="falcon1", eps=1e
 # device, which need not be the current one. Outputs and workspaces that a call makes are allocated on
 # `stream` (default: the device's current stream), where its kernels run.
 
-_NO_VIEW = (None, 0, 0, 0)
+_NO_VIEW = (0, 0, 0, 0)
 _HERE = contextlib.nullcontext()
 
 
@@ -409,14 +414,18 @@ def _seq(t, name, shape, dtype, dev):
 
 
 def _arr(t, name, shape, dtype, dev):
-    """Address of a contiguous parameter, state or gradient, or None."""
+    """Address of a contiguous parameter, state or gradient, or 0."""
     if t is None:
-        return None
+        return 0
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev):
         _refuse(t, name, shape, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _code(table, key, what) -> int:
@@ -433,11 +442,10 @@ def _call(name, *args):
 
 def _dense(shape, dtype, dev):
     """An uninitialised contiguous tensor."""
-    s, strides = 1, []
-    for n in reversed(shape):
-        strides.append(s)
-        s *= n if n > 1 else 1
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=dev)
+    strides = (1,)
+    for n in shape[:0:-1]:
+        strides = (n * strides[0],) + strides
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
 def _token_major(B, H, T, d, dev):
@@ -450,7 +458,8 @@ def _workspace(workspace, need, dev):
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
     _need(workspace, "workspace")
     if workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, other tensors on {dev}")
@@ -461,9 +470,9 @@ def _conv_args(x, w, bias, act, state, lengths, shape, state_shape, y, state_out
     dev, io, f32 = x.device, x.dtype, torch.float32
     B, H, d = shape[0], shape[1], shape[-1]
     K = w.shape[2]
-    return FalconConvArgs(
+    return _CONV_ARGS.pack(
         _dtype_code(x), B, H, shape[2] if len(shape) == 4 else 1, d, K, _code(ACTS, act, "act"),
-        _seq(x, "x", shape, io, dev), _seq(y, "y", shape, io, dev), _arr(w, "w", (H, d, K), f32, dev),
+        *_seq(x, "x", shape, io, dev), *_seq(y, "y", shape, io, dev), _arr(w, "w", (H, d, K), f32, dev),
         _arr(bias, "bias", (H, d), f32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev),
         _arr(state, "state", state_shape, io, dev), _arr(state_out, "state_out", state_shape, io, dev))
 
@@ -485,7 +494,7 @@ def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=
         if state_out is None and want_state:
             state_out = _dense(tail, x.dtype, x.device)
         a = _conv_args(x, w, bias, act, state, lengths, shape, tail, y, state_out)
-        _call("falcon_conv_fwd", ctypes.byref(a), raw)
+        _call("falcon_conv_fwd", a, raw)
     return y, state_out
 
 
@@ -501,7 +510,7 @@ def falcon_conv_step(x, w, state, *, bias=None, act="silu", state_out=None, y=No
             y = _dense(shape, x.dtype, x.device)
         a = _conv_args(x, w, bias, act, state, None, shape, (N, H, max(w.shape[2] - 1, 0), d), y,
                        state if state_out is None else state_out)
-        _call("falcon_conv_step", ctypes.byref(a), raw)
+        _call("falcon_conv_step", a, raw)
     return y
 
 
@@ -524,11 +533,11 @@ def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None
                "dbias": _dense((H, d), f32, dev) if bias is not None else None,
                "dstate": _dense(tail, f32, dev) if state is not None else None}
         a = _conv_args(x, w, bias, act, state, lengths, shape, tail, None, None)
-        g = FalconConvGrads(_seq(dy, "dy", shape, f32, dev), _arr(dstate_out, "dstate_out", tail, f32, dev),
-                            _seq(dx, "dx", shape, f32, dev), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"]))
-        need = int((_lib or lib()).falcon_conv_bwd_workspace_size(ctypes.byref(a)))
+        g = _CONV_GRADS.pack(*_seq(dy, "dy", shape, f32, dev), _arr(dstate_out, "dstate_out", tail, f32, dev),
+                             *_seq(dx, "dx", shape, f32, dev), _at(out["dw"]), _at(out["dbias"]), _at(out["dstate"]))
+        need = int((_lib or lib()).falcon_conv_bwd_workspace_size(a))
         workspace, p, n = _workspace(workspace, need, dev)
-        _call("falcon_conv_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+        _call("falcon_conv_bwd", a, g, p, n, raw)
     return out
 
 
@@ -545,10 +554,10 @@ def _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, len
     B, H, T, dk, dv = sizes
     dev, io, f32 = v.device, v.dtype, torch.float32
     state = (B, H, dv, dk)
-    return FalconScanArgs(
-        _dtype_code(v), B, H, T, dk, dv, FALCON_SCAN_SOFTPLUS if softplus else 0, _seq(q, "q", ks, io, dev),
-        _seq(k, "k", ks, io, dev), _seq(v, "v", vs, io, dev), _seq(delta, "delta", vs, io, dev), _seq(z, "z", vs, io, dev),
-        _seq(o, "o", vs, io, dev), _arr(A, "A", (H, dv, dk), f32, dev), _arr(D, "D", (H, dv), f32, dev),
+    return _SCAN_ARGS.pack(
+        _dtype_code(v), B, H, T, dk, dv, FALCON_SCAN_SOFTPLUS if softplus else 0, *_seq(q, "q", ks, io, dev),
+        *_seq(k, "k", ks, io, dev), *_seq(v, "v", vs, io, dev), *_seq(delta, "delta", vs, io, dev),
+        *_seq(z, "z", vs, io, dev), *_seq(o, "o", vs, io, dev), _arr(A, "A", (H, dv, dk), f32, dev), _arr(D, "D", (H, dv), f32, dev),
         _arr(delta_bias, "delta_bias", (H, dv), f32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev),
         _arr(S0, "S0", state, f32, dev), _arr(S_out, "S_out", state, f32, dev))
 
@@ -572,8 +581,9 @@ def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softp
         if S_out is None and want_state:
             S_out = _dense((B, H, dv, dk), torch.float32, dev)
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, o, S_out)
-        workspace, p, n = _workspace(workspace, falcon_scan_workspace_size(a) if workspace is None else 0, dev)
-        _call("falcon_scan_fwd", ctypes.byref(a), p, n, raw)
+        need = int((_lib or lib()).falcon_scan_workspace_size(a)) if workspace is None else 0
+        workspace, p, n = _workspace(workspace, need, dev)
+        _call("falcon_scan_fwd", a, p, n, raw)
     return o, S_out
 
 
@@ -587,7 +597,7 @@ def falcon_scan_step(q, k, v, delta, A, S, *, D=None, z=None, delta_bias=None, s
         if o is None:
             o = _dense(vs, v.dtype, v.device)
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, None, S, o, S if S_out is None else S_out)
-        _call("falcon_scan_step", ctypes.byref(a), raw)
+        _call("falcon_scan_step", a, raw)
     return o
 
 
@@ -609,12 +619,12 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
                "ddelta_bias": _dense((H, dv), f32, dev) if delta_bias is not None else None,
                "dS0": _dense((B, H, dv, dk), f32, dev) if S0 is not None else None}
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, None, None)
-        g = FalconScanGrads(_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev),
-                            *(_seq(out[n], n, s, f32, dev) for n, s in (("dq", ks), ("dk", ks), ("dv", vs), ("ddelta", vs), ("dz", vs))),
-                            *(_ptr(out[n]) for n in ("dA", "dD", "ddelta_bias", "dS0")))
-        need = int((_lib or lib()).falcon_scan_bwd_workspace_size(ctypes.byref(a)))
+        views = [x for n, s in (("dq", ks), ("dk", ks), ("dv", vs), ("ddelta", vs), ("dz", vs)) for x in _seq(out[n], n, s, f32, dev)]
+        g = _SCAN_GRADS.pack(*_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev), *views,
+                             _at(out["dA"]), _at(out["dD"]), _at(out["ddelta_bias"]), _at(out["dS0"]))
+        need = int((_lib or lib()).falcon_scan_bwd_workspace_size(a))
         workspace, p, n = _workspace(workspace, need, dev)
-        _call("falcon_scan_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+        _call("falcon_scan_bwd", a, g, p, n, raw)
     return out
 
 
@@ -634,9 +644,10 @@ def _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, 
     dev, io, f32 = x.device, x.dtype, torch.float32
     B, Hq, T, d = qs
     rot = int(rot)
-    return FalconQknormArgs(
+    return _QKNORM_ARGS.pack(
         _dtype_code(x), B, Hq, ks[1], T, d, _code(NORMS, norm, "norm"), rot, _code(ROTS, layout, "layout"),
-        _seq(q, "q", qs, io, dev), _seq(k, "k", ks, io, dev), _seq(q_out, "q_out", qs, io, dev), _seq(k_out, "k_out", ks, io, dev),
+        *_seq(q, "q", qs, io, dev), *_seq(k, "k", ks, io, dev), *_seq(q_out, "q_out", qs, io, dev),
+        *_seq(k_out, "k_out", ks, io, dev),
         _arr(wq, "wq", (d,), f32, dev), _arr(wk, "wk", (d,), f32, dev), float(eps), _arr(freq, "freq", (rot // 2,), f32, dev),
         _arr(positions, "positions", (B, T), torch.int32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev))
 
@@ -654,7 +665,7 @@ def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, la
         if k_out is None and k is not None:
             k_out = _dense(ks, x.dtype, x.device)
         a = _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
-        _call("falcon_qknorm_fwd", ctypes.byref(a), raw)
+        _call("falcon_qknorm_fwd", a, raw)
     return q_out, k_out
 
 
@@ -672,12 +683,12 @@ def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps
                "dwq": _dense(qs[3:], f32, dev) if wq is not None else None,
                "dwk": _dense(qs[3:], f32, dev) if wk is not None else None}
         a = _qknorm_args(x, qs, ks, q, k, None, None, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
-        g = FalconQknormGrads(_seq(dq_out, "dq_out", qs, f32, dev), _seq(dk_out, "dk_out", ks, f32, dev),
-                              _seq(out["dq"], "dq", qs, f32, dev), _seq(out["dk"], "dk", ks, f32, dev),
-                              _ptr(out["dwq"]), _ptr(out["dwk"]))
-        need = int((_lib or lib()).falcon_qknorm_bwd_workspace_size(ctypes.byref(a))) if wq is not None or wk is not None else 0
+        g = _QKNORM_GRADS.pack(*_seq(dq_out, "dq_out", qs, f32, dev), *_seq(dk_out, "dk_out", ks, f32, dev),
+                               *_seq(out["dq"], "dq", qs, f32, dev), *_seq(out["dk"], "dk", ks, f32, dev),
+                               _at(out["dwq"]), _at(out["dwk"]))
+        need = int((_lib or lib()).falcon_qknorm_bwd_workspace_size(a)) if wq is not None or wk is not None else 0
         workspace, p, n = _workspace(workspace, need, dev)
-        _call("falcon_qknorm_bwd", ctypes.byref(a), ctypes.byref(g), p, n, raw)
+        _call("falcon_qknorm_bwd", a, g, p, n, raw)
     return out
 
 

@@ -38,6 +38,33 @@ def test_struct_layout_matches_header(tmp_path, mirror, ctype):
     assert ctypes.sizeof(mirror) == int(got["sizeof"])
 
 
+@pytest.mark.parametrize("packer,mirror", [
+    (F._CONV_ARGS, F.FalconConvArgs), (F._CONV_GRADS, F.FalconConvGrads), (F._SCAN_ARGS, F.FalconScanArgs),
+    (F._SCAN_GRADS, F.FalconScanGrads), (F._QKNORM_ARGS, F.FalconQknormArgs), (F._QKNORM_GRADS, F.FalconQknormGrads)])
+def test_packed_structs_are_the_mirrors(packer, mirror):
+    """The calls pack their structs as bytes: the same layout, field by field."""
+    flat, count = [], iter(range(1, 1000))
+
+    def fill(s):
+        for name, kind in s._fields_:
+            if kind is F.FalconView:
+                fill(getattr(s, name))
+            else:
+                x = next(count)
+                setattr(s, name, x)
+                flat.append(float(x) if kind is ctypes.c_float else x)
+
+    s = mirror()
+    fill(s)
+    packed = packer.pack(*flat)
+    assert len(packed) == ctypes.sizeof(mirror)
+    assert bytes(mirror.from_buffer_copy(packed)) == packed
+    again = mirror.from_buffer_copy(packed)
+    same = lambda a, b: all(same(getattr(a, n), getattr(b, n)) if k is F.FalconView else getattr(a, n) == getattr(b, n)
+                            for n, k in a._fields_)
+    assert same(s, again)
+
+
 def view(p, B, H, T, d):
     return F.FalconView(p, H * T * d, T * d, d)
 
