@@ -9,16 +9,23 @@ constexpr int kSumCols = 32, kChains = 8;
 
 struct SumJobs {
     SumJob job[4];
+    unsigned first[4];   // blocks of the jobs before
+    int count;
 };
 
-// 32 columns a block (one 128-byte line of each row), kChains sums over every kChains-th row, joined in a
-// fixed order. Bound by the latency of the loads: eight rows of a chain are in flight together. 33000 columns of 128
-// rows take 16.5 us, 128 columns of 296 rows 6 us (with 32 chains and blocks of 1024 threads 52 and 6.7 us).
+// 32 columns a block (one 128-byte line of each row), kChains sums over every kChains-th row, joined in a fixed order.
+// Bound by the latency of the loads: eight rows of a chain are in flight together. 36900 columns of 26 rows take 4.1 us,
+// 10240 of 108 rows 4.7 us, 256 of 296 rows 5.7 us (one chain and 128 columns a block: 5.1, 9.1 and 18 us; 32 chains:
+// slower by a tenth to threefold). Blocks are numbered through the jobs: a grid of the widest job for each of them
+// took 16 us for the first of these.
 __global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs jobs, int nparts) {
     __shared__ float acc[kChains][kSumCols + 1];
-    const SumJob j = jobs.job[blockIdx.y];
-    if ((long long)blockIdx.x * kSumCols >= j.n) return;
-    const long long e = (long long)blockIdx.x * kSumCols + threadIdx.x;
+    int which = 0;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        if (i < jobs.count && blockIdx.x >= jobs.first[i]) which = i;
+    const SumJob j = jobs.job[which];
+    const long long e = (long long)(blockIdx.x - jobs.first[which]) * kSumCols + threadIdx.x;
     float s = 0.f;
     if (e < j.n) {
         constexpr int U = 8;
@@ -53,17 +60,16 @@ __global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs 
 
 cudaError_t launch_column_sums(const SumJob *jobs, int njobs, long long nparts, cudaStream_t s) {
     SumJobs js{};
-    long long most = 0;
-    int n = 0;
+    long long blocks = 0;
     for (int i = 0; i < njobs; ++i) {
         if (!jobs[i].out || jobs[i].n == 0) continue;
-        js.job[n++] = jobs[i];
-        most = jobs[i].n > most ? jobs[i].n : most;
+        js.job[js.count] = jobs[i];
+        js.first[js.count++] = (unsigned)blocks;
+        blocks += (jobs[i].n + kSumCols - 1) / kSumCols;
     }
-    if (n == 0) return cudaSuccess;
-    if (nparts > 0x7fffffff / 16) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)((most + kSumCols - 1) / kSumCols), (unsigned)n);
-    column_sum_kernel<<<grid, dim3(kSumCols, kChains), 0, s>>>(js, (int)nparts);
+    if (js.count == 0) return cudaSuccess;
+    if (blocks > kMaxGrid || nparts > 0x7fffffff / 16) return cudaErrorInvalidConfiguration;
+    column_sum_kernel<<<(unsigned)blocks, dim3(kSumCols, kChains), 0, s>>>(js, (int)nparts);
     return cudaGetLastError();
 }
 

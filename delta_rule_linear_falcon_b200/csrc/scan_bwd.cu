@@ -29,7 +29,6 @@ namespace {
 constexpr int kSub = 4;              // tokens whose states are kept in registers
 constexpr int kNSub = 4;
 constexpr int kSeg = kSub * kNSub;   // tokens of a segment
-constexpr int kBlockTokens = 64;     // tokens that a block of step 1 takes, or one walk
 
 template <int SL> struct BwdShape {
     static constexpr int kWarps = SL == 1 ? 1 : (SL == 2 ? 2 : 4);
@@ -541,14 +540,18 @@ int bwd_channels(int sl) {
 
 struct BwdSizes {
     int nseg, walk, nwalk, ngrp, cols;
+    int block;          // walks of a block of step 1
     long long rows;     // channels of all sequences
     long long qk;       // floats of all parts of dq and dk
     long long floats;   // the workspace
 };
 
-// Segments of a walk: as many as leave four blocks of step 3 for each place on an SM. Long walks make few joins, and
-// few parts of dA (each as large as the state): 437 us in all with one segment for the case above, 385 with two, 382
-// with four, 470 with eight, whose blocks no longer fill the SMs.
+// Turns that `blocks` blocks take at three an SM (what the registers of steps 1 and 3 allow).
+long long turns(long long blocks) { return (blocks + 148 * 3 - 1) / (148 * 3); }
+
+// Segments of a walk: those with the shortest estimate in tokens' work of a block of step 3: its turns times a walk and
+// its prologue, and 0.4 for each walk's joins and parts of dA (as large as the state). For the case above that is ten
+// segments, one turn of 416 blocks: 344 us in all; with two, four and eight it took 385, 382 and 470.
 BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     BwdSizes z;
     z.nseg = (a.T + kSeg - 1) / kSeg;
@@ -556,9 +559,29 @@ BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     z.ngrp = (a.dv + ch - 1) / ch;
     z.cols = scan_cols(a.dk);
     z.rows = (long long)a.B * a.H * a.dv;
+    const long long groups = (long long)z.ngrp * a.B * a.H;
+    double best = 0.0;
     z.walk = 1;
-    while (z.walk < 16 && (long long)z.ngrp * a.B * a.H * ((z.nseg + 2 * z.walk - 1) / (2 * z.walk)) >= 148 * 12) z.walk *= 2;
+    for (int walk = 1; walk <= 32; ++walk) {
+        const long long n = (z.nseg + walk - 1) / walk;
+        const double cost = (double)turns(groups * n) * (walk * kSeg + 4) + 0.4 * n;
+        if (walk == 1 || cost < best) {
+            best = cost;
+            z.walk = walk;
+        }
+    }
     z.nwalk = (z.nseg + z.walk - 1) / z.walk;
+    // step 1: blocks of as many walks as fill the SMs best, with a prologue of about 24 tokens' time
+    const int cpb = kScanThreads / (a.dk <= 16 ? 1 : a.dk <= 32 ? 2 : a.dk <= 64 ? 4 : 8);
+    const long long groups1 = (long long)a.B * a.H * ((a.dv + cpb - 1) / cpb);
+    z.block = 1;
+    for (int n = 1; n <= 16; ++n) {
+        const double cost = (double)turns(groups1 * ((z.nwalk + n - 1) / n)) * (n * z.walk * kSeg + 24);
+        if (n == 1 || cost < best) {
+            best = cost;
+            z.block = n;
+        }
+    }
     z.qk = z.ngrp > 1 ? 2LL * z.ngrp * a.B * a.H * a.T * a.dk : 0;
     z.floats = z.rows * (z.nseg * (z.cols + 1LL) + z.nwalk * (2LL * z.cols + 1 + a.dk + 2)) + z.qk;
     return z;
@@ -599,7 +622,7 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
     w.s.nseg = z.nseg;
     w.s.walk = z.walk;
     w.s.nwalk = z.nwalk;
-    w.s.block = z.walk * kSeg >= kBlockTokens ? 1 : kBlockTokens / (z.walk * kSeg);
+    w.s.block = z.block;
     w.s.dO = g.dO;
     w.s.ends = ws;   // the rows of states first: they are read as 16-byte pairs
     w.s.wends = w.s.ends + z.nseg * z.rows * z.cols;
