@@ -359,6 +359,6 @@ falcon_status_t falcon_debug_stall_next_call(int block, long long wait_budget_cy
     return FALCON_OK;
 }
 
-int falcon_version(void) { return 100; }
+int falcon_version(void) { return 200; }
 
 }  // extern "C"

@@ -15,7 +15,7 @@
 // dp_t x to dw, and emits dx_{t-K+1} = sum_j w_j dp_{t-j}. The walk goes K - 1 tokens past the run
 // (dp there is formed again by the next run). dw and dbias: registers, then the block's shared memory,
 // then one row of partial sums for each block, summed in a fixed order by a second launch. B4 H16 T4096 d128 bf16:
-// 71 us and 7 us for 336 MB (51 us at the copy rate), 144 us in all off alignment.
+// 71 us and 5 us of kernels for 336 MB (51 us at the copy rate), 144 us in all off alignment.
 #include "ops.cuh"
 
 namespace falcon {
@@ -37,7 +37,7 @@ struct ConvShape {
 
 // Runs: so long that the blocks fill the `slots` that the SMs hold once, twice, .. (long runs re-read less of the past
 // and leave fewer partial rows; a part-filled last turn costs as much as a full one: 55 us against 57 forward and 84
-// against 89 backward for a fixed 128), and at most kLongest tokens.
+// against 89 backward with runs of 128), and at most kLongest tokens.
 ConvShape conv_shape(const falcon_conv_args_t &a, int V, long long slots) {
     constexpr long long kLongest = 160, kShortest = 8;
     ConvShape s;

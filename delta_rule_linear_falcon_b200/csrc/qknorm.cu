@@ -12,7 +12,7 @@
 // Where pointers, strides, d or rot are not multiples of a pack, V = 1: lane l owns channels l, l + 32, ..
 // and partners come through shared memory (the same case with rows off alignment: 255 us against 98).
 // Backward: the same walk with the row turned back; dwq and dwk are summed per lane over the tokens of a
-// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 47 us and 6 us for 210 MB (32 us at the copy rate);
+// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 47 us and 6 us of kernels for 210 MB (32 us at the copy rate);
 // bound by instruction latency, 16 warps an SM (the registers of two rows and their prefetch).
 #include "ops.cuh"
 

@@ -11,7 +11,7 @@
 // as 16-byte asynchronous copies into a ring in shared memory, one copy a thread and tensor, and are read there at
 // fixed offsets; o goes back the same way, in the place of z (or v) (loads and stores of single elements, with
 // their addresses, took a fifth of the pass). Where rows are not 16-byte multiples, elements are copied one by one
-// (B1 T16384 dv2048 off alignment: 511 us against 370).
+// (B1 T16384 dv2048 off alignment: 511 us where this took 370).
 // q_t and k_t, the same for all channels of a head, are staged in fp32 and read as broadcasts. Step sizes (softplus)
 // are computed two tokens an instruction, once per channel and token.
 //
@@ -19,9 +19,10 @@
 // cut into segments (scan_plan). A first launch runs every segment from a zero state and leaves its end
 // state E and the sum of its steps sd, from which the decay over the segment is exp(A sd); in the second
 // each segment joins the states before it, S <- exp(A sd_j) S + E_j, and runs with outputs.
-// Measured, bf16, dk = 16: B4 H16 T2048 dv128 (64 blocks unsplit) 196 us in 9 segments, 398 us unsplit; the
-// exponential unit is at 81% in the first launch and 72% in the second. B1 T16384 dv2048: 370 us in 37 segments. 512
-// blocks unsplit (B32 H16 T1024 dv128): 458 us, 115 us for each 2^28 entries, whose exponentials alone are 58 us.
+// Measured, bf16, dk = 16: B4 H16 T2048 dv128 (64 blocks unsplit) 183 us in 9 segments (unsplit, with the exponentials
+// of an earlier step-size formula, 398 us where 9 segments took 204); the exponential unit is at about 80% in the first
+// launch and 70% in the second. B1 T16384 dv2048: 352 us in 37 segments. 512 blocks unsplit (B32 H16 T1024 dv128,
+// the earlier formula): 458 us, 115 us for each 2^28 entries, whose exponentials alone are 58 us.
 #include "scan.cuh"
 
 namespace falcon {

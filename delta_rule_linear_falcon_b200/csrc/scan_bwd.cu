@@ -16,7 +16,7 @@
 // Step 3 sums over channels (dq, dk) and over columns (dv, ddelta, dz) of the same products. A thread owns
 // 4 channels x 4 columns, SL = dk / 4 lanes side by side: the first additions of either sum are fused
 // multiply-adds in registers, the rest 3 to 6 shuffles (lanes_sum) for 16 entries.
-// B2 H16 T2048 dv128 dk16, bf16: 82 us for step 1, 30 for the joins, 255 for step 3, 17 for the sums. Step 3 is bound by
+// B2 H16 T2048 dv128 dk16, bf16, 332 us: 75 us for step 1, 12 for the joins, 258 for step 3 (alone), 4 for the sums. Step 3 is bound by
 // latency at 12 warps an SM (168 registers, half of them states; 70 KB of shared memory): its instruction slots are at
 // half, the exponential unit at 40%. Taken out one at a time, the channels' gradients at a segment's end were 55 us of it
 // (45 since they are formed two tokens an instruction), the shuffled sums 28, the exponentials 19.
@@ -551,7 +551,7 @@ long long turns(long long blocks) { return (blocks + 148 * 3 - 1) / (148 * 3); }
 
 // Segments of a walk: those with the shortest estimate in tokens' work of a block of step 3: its turns times a walk and
 // its prologue, and 0.4 for each walk's joins and parts of dA (as large as the state). For the case above that is ten
-// segments, one turn of 416 blocks: 344 us in all; with two, four and eight it took 385, 382 and 470.
+// segments, one turn of 416 blocks (with two, four and eight segments 385, 382 and 470 us in all where this took 344).
 BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     BwdSizes z;
     z.nseg = (a.T + kSeg - 1) / kSeg;
