@@ -263,7 +263,7 @@ struct False { static constexpr bool value = false; };
 
 template <typename IO, int K, int V, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(falcon_conv_args_t a, falcon_conv_grads_t g, ConvShape s,
-                                                                   float *part) {
+                                                                   float *part_w, float *part_b) {
     typedef Pack<IO, V> P;
     typedef Pack<float, V> F;
     constexpr int kPast = Taps<K>::kPast, N = Pairs<V>::N;
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(
         copy_wait<0>();
     }
     __syncthreads();   // the rings' places are free
-    // the block's sums over its runs, then one partial row: (H,d,K) of dw, (H,d) of dbias
+    // the block's sums over its runs, then one partial row of dw (H,d,K) and of dbias (H,d)
     constexpr int M = (K + 1) * V;
     float *sums = reinterpret_cast<float *>(smem);
     float *mine = sums + me * M;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(
     }
     __syncthreads();
     const long long HD = (long long)a.H * a.d;
-    float *row = part + ((long long)b * s.ntb + tb) * HD * (K + 1);
+    const long long row = (long long)b * s.ntb + tb;
     for (int e = me; e < s.bx * M; e += kConvThreads) {
         float acc = 0.f;
         for (int y = 0; y < s.by; ++y) acc += sums[(long long)y * s.bx * M + e];
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(kConvThreads, K <= 4 ? 3 : 2) conv_bwd_kernel(
         if (pk >= (long long)a.H * s.nv) continue;
         const int m = e % M;
         const long long c = pk / s.nv * a.d + pk % s.nv * V;
-        if (m < K * V) row[c * K + m] = acc;
-        else row[HD * K + c + (m - K * V)] = acc;
+        if (m < K * V) part_w[(row * HD + c) * K + m] = acc;
+        else part_b[row * HD + c + (m - K * V)] = acc;
     }
 }
 
@@ -513,7 +513,7 @@ cudaError_t conv_step_io(const falcon_conv_args_t &a, cudaStream_t st) {
 }
 
 template <typename IO, int V>
-cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &g, const ConvShape &s, float *ws, cudaStream_t st) {
+cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &g, const ConvShape &s, float *pw, float *pb, cudaStream_t st) {
     const long long blocks = s.ncb * s.ntb * a.B;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const dim3 block(s.bx, s.by);
@@ -527,7 +527,7 @@ cudaError_t conv_bwd_io(const falcon_conv_args_t &a, const falcon_conv_grads_t &
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); \
             if (e != cudaSuccess) return e;                                                       \
         }                                                                                         \
-        kern<<<(unsigned)blocks, block, smem, st>>>(a, g, s, ws);                                 \
+        kern<<<(unsigned)blocks, block, smem, st>>>(a, g, s, pw, pb);                                 \
     }
     FALCON_CONV_TAPS(FALCON_RUN)
 #undef FALCON_RUN
@@ -571,15 +571,18 @@ cudaError_t launch_conv_bwd(const falcon_conv_args_t &a, const falcon_conv_grads
     if (a.H == 0) return cudaSuccess;
     const int V = conv_pack(a, &g.dy, &g.dx);
     const ConvShape s = conv_bwd_shape(a, V);
+    // partial rows of dw, then of dbias; a single one is the gradient
+    const long long HD = (long long)a.H * a.d, rows = (long long)a.B * s.ntb;
+    float *pw = rows == 1 ? g.dw : ws, *pb = rows == 1 && g.dbias ? g.dbias : ws + rows * HD * a.K;
     if (a.B > 0) {
         cudaError_t e;
-        if (a.io_dtype == FALCON_BF16) e = V == 2 ? conv_bwd_io<__nv_bfloat16, 2>(a, g, s, ws, st) : conv_bwd_io<__nv_bfloat16, 1>(a, g, s, ws, st);
-        else e = V == 2 ? conv_bwd_io<float, 2>(a, g, s, ws, st) : conv_bwd_io<float, 1>(a, g, s, ws, st);
+        if (a.io_dtype == FALCON_BF16) e = V == 2 ? conv_bwd_io<__nv_bfloat16, 2>(a, g, s, pw, pb, st) : conv_bwd_io<__nv_bfloat16, 1>(a, g, s, pw, pb, st);
+        else e = V == 2 ? conv_bwd_io<float, 2>(a, g, s, pw, pb, st) : conv_bwd_io<float, 1>(a, g, s, pw, pb, st);
         if (e != cudaSuccess) return e;
     }
-    const long long HD = (long long)a.H * a.d, row = HD * (a.K + 1);   // dw (H,d,K), then dbias (H,d)
-    const SumJob jobs[2] = {{ws, HD * a.K, row, g.dw}, {ws + HD * a.K, HD, row, g.dbias}};
-    return launch_column_sums(jobs, 2, (long long)a.B * s.ntb, st);
+    if (rows == 1) return cudaSuccess;
+    const SumJob jobs[2] = {{pw, HD * a.K, HD * a.K, g.dw}, {pb, HD, HD, g.dbias}};
+    return launch_column_sums(jobs, 2, rows, st);
 }
 
 }  // namespace falcon

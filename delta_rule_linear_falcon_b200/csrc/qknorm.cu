@@ -23,7 +23,7 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kMaxWidth = 256;
-constexpr double kInvTwoPi = 0.15915494309189533577;
+constexpr double kTwoOverPi = 0.63661977236758134308;
 
 struct NormShape {
     long long groups;   // ceil(B T / tokens of a block): one token for each group of lanes
@@ -50,6 +50,24 @@ __host__ __device__ inline int turn_slots(const falcon_qknorm_args_t &a, int V) 
     return V == 1 ? a.rot / 2 : (a.rot + V - 1) / V * (V / 2);
 }
 
+// (cos, sin) of t quarter turns: whole ones are taken off in fp64, and the rest f, |f| <= 1/2, goes into polynomials in
+// f^2 for sin(f pi/2) / f and cos(f pi/2) (least-squares fits on [0, 1/4], good to 3e-9). With few heads a token's
+// angles are a fifth of its work, and the library's sine and cosine took twice the instructions.
+__device__ __forceinline__ float2 turned(double t) {
+    const double whole = rint(t);
+    const float f = (float)(t - whole), u = f * f;
+    float s = fmaf(u, -0.0046016579f, 0.079680033f);
+    s = fmaf(u, s, -0.64596349f);
+    s = f * fmaf(u, s, 1.5707964f);
+    float c = fmaf(u, 0.00090402167f, -0.020860288f);
+    c = fmaf(u, c, 0.25366923f);
+    c = fmaf(u, c, -1.2337005f);
+    c = fmaf(u, c, 1.f);
+    const int q = (int)__double2ll_rn(whole) & 3;
+    const float x = q & 1 ? -s : c, y = q & 1 ? c : s;
+    return q & 2 ? make_float2(-x, -y) : make_float2(x, y);
+}
+
 // Sines and cosines of `tokens` tokens from tok0 on. Padded pairs turn by nothing.
 template <int V>
 __device__ __forceinline__ void angles(const falcon_qknorm_args_t &a, long long tok0, int tokens, float2 *cs) {
@@ -61,8 +79,7 @@ __device__ __forceinline__ void angles(const falcon_qknorm_args_t &a, long long 
         float2 r = make_float2(1.f, 0.f);
         if (tok < all && p < half) {
             const double pos = a.positions ? (double)a.positions[tok] : (double)(tok % a.T);
-            const double turns = pos * (double)a.freq[p] * kInvTwoPi;
-            sincospif(2.f * (float)(turns - rint(turns)), &r.y, &r.x);
+            r = turned(pos * (double)a.freq[p] * kTwoOverPi);
         }
         cs[j * slots + turn_slot<V>(a, p)] = r;
     }
@@ -203,7 +220,7 @@ template <typename IO, int V, int LANES, int NV, bool HALF>
 __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_args_t a, NormShape s) {
     typedef Row<IO, V, HALF> R;
     constexpr int G = kNormThreads / LANES;       // groups of lanes, tokens of a block
-    constexpr int kRows = V == 1 ? 1 : 4 / NV;    // rows in flight
+    constexpr int kRows = NV >= 4 ? 1 : 4 / NV;   // rows in flight
     extern __shared__ __align__(16) float2 cs[];
     __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
     float *stage = stage_all[V == 1 ? threadIdx.x >> 5 : 0];
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
     typedef Row<IO, V, HALF> R;
     typedef Row<float, V, HALF> F;
     constexpr int G = kNormThreads / LANES;
-    constexpr int kRows = V == 1 || NV > 1 ? 1 : 2;   // rows worked on together, as many more on their way
+    constexpr int kRows = NV > 1 ? 1 : 2;   // rows worked on together, as many more on their way
     extern __shared__ __align__(16) float2 cs[];
     __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
     __shared__ float sw[2][kMaxWidth];
@@ -518,14 +535,19 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
         part[(long long)blockIdx.x * 2 * a.d + i] = sw[i / a.d][i % a.d];
 }
 
-// The pack's width: 16 bytes of the io type where every row and the rotation allow it (accesses are of half a pack).
+// The pack's width: 16 bytes of the io type where every row and the rotation allow it (accesses are of half a pack), for
+// bf16 also 8; else one channel.
 int norm_pack(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g) {
-    const int es = a.io_dtype == FALCON_BF16 ? 2 : 4, V = 16 / es, H = V / 2;
-    bool ok = a.d % V == 0 && view_packs(a.q, H, es) && view_packs(a.k, H, es);
-    if (a.rot_layout == FALCON_ROT_HALF) ok = ok && a.rot % V == 0;
-    if (!g) ok = ok && view_packs(a.q_out, H, es) && view_packs(a.k_out, H, es);
-    else ok = ok && view_packs(g->dq_out, H, 4) && view_packs(g->dk_out, H, 4) && view_packs(g->dq, H, 4) && view_packs(g->dk, H, 4);
-    return ok ? V : 1;
+    const int es = a.io_dtype == FALCON_BF16 ? 2 : 4;
+    for (int V = 16 / es; V >= 4; V /= 2) {
+        const int H = V / 2;
+        bool ok = a.d % V == 0 && view_packs(a.q, H, es) && view_packs(a.k, H, es);
+        if (a.rot_layout == FALCON_ROT_HALF) ok = ok && a.rot % V == 0;
+        if (!g) ok = ok && view_packs(a.q_out, H, es) && view_packs(a.k_out, H, es);
+        else ok = ok && view_packs(g->dq_out, H, 4) && view_packs(g->dk_out, H, 4) && view_packs(g->dq, H, 4) && view_packs(g->dk, H, 4);
+        if (ok) return V;
+    }
+    return 1;
 }
 
 int norm_lanes(const falcon_qknorm_args_t &a, int V) {
@@ -567,17 +589,30 @@ cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t 
     return cudaGetLastError();
 }
 
+template <typename IO, int V, bool HALF>
+cudaError_t norm_packed(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
+    if constexpr (V < 8) {   // 256 channels of 8 are 32 packs
+        if (a.d / V > 32) return norm_run<IO, V, 32, 2, HALF>(a, g, part, st);
+    }
+    switch (norm_lanes(a, V)) {
+        case 4: return norm_run<IO, V, 4, 1, HALF>(a, g, part, st);
+        case 8: return norm_run<IO, V, 8, 1, HALF>(a, g, part, st);
+        case 16: return norm_run<IO, V, 16, 1, HALF>(a, g, part, st);
+        default: return norm_run<IO, V, 32, 1, HALF>(a, g, part, st);
+    }
+}
+
 template <typename IO, int W, bool HALF>
 cudaError_t norm_io(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
     const int V = norm_pack(a, g);
-    if (V == 1) return norm_run<IO, 1, 32, 8, HALF>(a, g, part, st);
-    if (a.d / V > 32) return norm_run<IO, W, 32, 2, HALF>(a, g, part, st);
-    switch (norm_lanes(a, V)) {
-        case 4: return norm_run<IO, W, 4, 1, HALF>(a, g, part, st);
-        case 8: return norm_run<IO, W, 8, 1, HALF>(a, g, part, st);
-        case 16: return norm_run<IO, W, 16, 1, HALF>(a, g, part, st);
-        default: return norm_run<IO, W, 32, 1, HALF>(a, g, part, st);
+    if (V == W) return norm_packed<IO, W, HALF>(a, g, part, st);
+    if constexpr (W == 8) {
+        if (V == 4) return norm_packed<IO, 4, HALF>(a, g, part, st);
     }
+    if (a.d <= 32) return norm_run<IO, 1, 32, 1, HALF>(a, g, part, st);
+    if (a.d <= 64) return norm_run<IO, 1, 32, 2, HALF>(a, g, part, st);
+    if (a.d <= 128) return norm_run<IO, 1, 32, 4, HALF>(a, g, part, st);
+    return norm_run<IO, 1, 32, 8, HALF>(a, g, part, st);
 }
 
 cudaError_t norm_any(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {

@@ -13,6 +13,7 @@
 //      time, their states again into registers and G backward;
 //   4. sums of partial rows: dA, dD, ddelta_bias over walks and sequences, dq and dk over the blocks of a head's
 //      channels, in a fixed order.
+// A sequence that is one walk needs no joins, one that is one segment no step 1 either.
 // Step 3 sums over channels (dq, dk) and over columns (dv, ddelta, dz) of the same products. A thread owns
 // 4 channels x 4 columns, SL = dk / 4 lanes side by side: the first additions of either sum are fused
 // multiply-adds in registers, the rest 3 to 6 shuffles (lanes_sum) for 16 entries.
@@ -103,7 +104,10 @@ __global__ void __launch_bounds__(256) scan_join_kernel(falcon_scan_args_t a, Sc
     }
 }
 
-template <typename IO, int SL>
+// ONE: the sequence is a single walk, so that its states are the given ones and its gradient of the initial state the
+// answer, and a segment's sub-segments without tokens are passed over (B3 H16 T5 dk32 dv2048: 117 us in all against 373).
+// Compiled on its own, because the registers it takes cost the other 355 us instead of 332 for the case above.
+template <typename IO, int SL, bool ONE>
 __global__ void __launch_bounds__(BwdShape<SL>::kThreads, BwdShape<SL>::kWarps == 4 ? 3 : 1)
 scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int ngrp) {
     typedef BwdShape<SL> Sh;
@@ -170,11 +174,20 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
             for (int s = 0; s < 4; ++s) S[i][s] = fma2(ex2_2(mul2(dt[i], A2[i][s])), S[i][s], mul2(dtv[i], k[s]));
     };
 
+    // a row of (B,H,dv,dk): this thread's columns
+    auto given = [&](const float *s, long long row, f32x2 (&o)[2]) {
+        float v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = s && sl * 4 + c < a.dk ? s[row * a.dk + sl * 4 + c] : 0.f;
+        o[0] = pack2(v[0], v[1]);
+        o[1] = pack2(v[2], v[3]);
+    };
     const int seg0 = walk * w.s.walk, seg1 = min(seg0 + w.s.walk, w.s.nseg);
 #pragma unroll 1
     for (int seg = seg1 - 1; seg >= seg0; --seg) {
         const int t0 = seg * kSeg;
         const int here = min(max(n - t0, 0), kSeg), rows = min(a.T - t0, kSeg);   // tokens of the sequence; of the arrays
+        const int subs = ONE ? max((here + kSub - 1) / kSub, 1) : kNSub;   // sub-segments to go through
         // ---- the segment's states (a row of each channel), then its inputs
         {
             f32x2 x[4][2], y[4][2], u[4][2];
@@ -186,10 +199,17 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
                 pre[i] = 0.f;
                 if (ch < a.dv) {
                     const long long row = (long long)bh * a.dv + ch;
-                    load_pairs(w.s.ends + (row * w.s.nseg + seg) * COLS + sl * 4, x[i][0], x[i][1]);
-                    load_pairs(w.s.wends + (row * w.s.nwalk + walk) * COLS + sl * 4, y[i][0], y[i][1]);
-                    pre[i] = w.s.steps[row * w.s.nseg + seg];
-                    if (seg == seg1 - 1) load_pairs(w.s.wgrads + (row * w.s.nwalk + walk) * COLS + sl * 4, u[i][0], u[i][1]);
+                    if (!ONE || w.s.nseg > 1) {   // a single one starts its walk
+                        load_pairs(w.s.ends + (row * w.s.nseg + seg) * COLS + sl * 4, x[i][0], x[i][1]);
+                        pre[i] = w.s.steps[row * w.s.nseg + seg];
+                    }
+                    if (ONE) {
+                        given(a.S0, row, y[i]);
+                        if (seg == seg1 - 1) given(g.dS_T, row, u[i]);
+                    } else {
+                        load_pairs(w.s.wends + (row * w.s.nwalk + walk) * COLS + sl * 4, y[i][0], y[i][1]);
+                        if (seg == seg1 - 1) load_pairs(w.s.wgrads + (row * w.s.nwalk + walk) * COLS + sl * 4, u[i][0], u[i][1]);
+                    }
                 }
             }
             const IO *pk = row_of<IO>(a.k, b, h, t0), *pq = row_of<IO>(a.q, b, h, t0);
@@ -302,7 +322,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
                 for (int s = 0; s < (CL >= 4 ? 1 : 4 / CL); ++s) sDq[(warp * kSeg + t) * COLS + sl * 4 + iq + s] = dq[s];
         };
 #pragma unroll 1
-        for (int t = 0; t < kSeg - kSub; ++t) {
+        for (int t = 0; t < (subs - 1) * kSub; ++t) {
             if (t % kSub == 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -314,9 +334,9 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
 
         // ---- sub-segment by sub-segment from the end: the states before its tokens, then backward
 #pragma unroll 1
-        for (int sub = kNSub - 1; sub >= 0; --sub) {
+        for (int sub = subs - 1; sub >= 0; --sub) {
             f32x2 before[kSub][2][4];
-            const bool last = sub == kNSub - 1;   // its forward pass is still to come
+            const bool last = sub == subs - 1;    // its forward pass is still to come
             if (!last) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -440,7 +460,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
                     const bool in0 = j0 + u < here, in1 = j0 + u + 1 < here;   // rows behind the end are 0
                     l0 = in0 ? l0 : 0.f;
                     l1 = in1 ? l1 : 0.f;
-                    dd2 = fma2(dy, v, dd2);     // dy is 0 there
+                    dd2 = fma2(dy, v, dd2);     // dy and v are 0 there
                     db2 = add2(db2, pack2(l0, l1));
                     if (j0 + u < rows) {
                         *ov = in0 ? d0 : 0.f;
@@ -465,10 +485,12 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
             const int j = idx / COLS, c = idx % COLS;
             if (j >= rows || c >= a.dk) continue;
             float dq = 0.f, dk = 0.f;
+            if (j < here) {
 #pragma unroll
-            for (int x = 0; x < Sh::kWarps; ++x) {
-                dq += sDq[(x * kSeg + j) * COLS + c];
-                dk += sDk[(x * kSeg + j) * COLS + c];
+                for (int x = 0; x < Sh::kWarps; ++x) {
+                    dq += sDq[(x * kSeg + j) * COLS + c];
+                    dk += sDk[(x * kSeg + j) * COLS + c];
+                }
             }
             if (ngrp == 1) {
                 row_of<float>(g.dq, b, h, t0 + j)[c] = dq;
@@ -494,6 +516,12 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
             float *to = w.dA + (part * HV + (long long)h * a.dv + ch) * a.dk + c;
             if (ch < a.dv && c < a.dk) to[0] = lo;
             if (ch + 1 < a.dv && c < a.dk) to[a.dk] = hi;
+            if (ONE && g.dS0) {   // G has come down to the initial state
+                float *to_s = g.dS0 + ((long long)bh * a.dv + ch) * a.dk + c;
+                unpack2(G[i][s], lo, hi);
+                if (ch < a.dv && c < a.dk) to_s[0] = lo;
+                if (ch + 1 < a.dv && c < a.dk) to_s[a.dk] = hi;
+            }
         }
 #pragma unroll
     for (int m = 0; m < Sh::kPer; ++m) {
@@ -592,9 +620,10 @@ cudaError_t scan_bwd_t(const falcon_scan_args_t &a, const falcon_scan_grads_t &g
     const long long blocks = (long long)ngrp * a.B * a.H * w.s.nwalk;
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const size_t smem = BwdShape<SL>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<IO, SL>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto kern = w.s.nwalk == 1 ? scan_bwd_kernel<IO, SL, true> : scan_bwd_kernel<IO, SL, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    scan_bwd_kernel<IO, SL><<<(unsigned)blocks, BwdShape<SL>::kThreads, smem, s>>>(a, g, w, ngrp);
+    kern<<<(unsigned)blocks, BwdShape<SL>::kThreads, smem, s>>>(a, g, w, ngrp);
     return cudaGetLastError();
 }
 
@@ -633,17 +662,25 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
     w.dd = w.dA + z.nwalk * z.rows * a.dk;
     w.db = w.dd + z.nwalk * z.rows;
     w.qk = w.db + z.nwalk * z.rows;
+    const bool single = z.nwalk == 1 && a.B == 1;   // one part of each parameter's gradient: it is the gradient
+    if (single) {
+        w.dA = g.dA;
+        if (g.dD) w.dd = g.dD;
+        if (g.ddelta_bias) w.db = g.ddelta_bias;
+    }
     cudaError_t e;
     if (a.B > 0) {
-        if (z.nseg > 0) {
+        if (z.nseg > 1) {
             e = launch_scan_pass(kScanBoth, a, w.s, s);
             if (e != cudaSuccess) return e;
         }
-        const long long jb = (z.rows * z.cols + 255) / 256;
-        if (jb > kMaxGrid) return cudaErrorInvalidConfiguration;
-        scan_join_kernel<<<dim3((unsigned)jb, 2), 256, 0, s>>>(a, w.s, z.cols, g.dS_T, g.dS0);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if (z.nwalk != 1) {
+            const long long jb = (z.rows * z.cols + 255) / 256;
+            if (jb > kMaxGrid) return cudaErrorInvalidConfiguration;
+            scan_join_kernel<<<dim3((unsigned)jb, 2), 256, 0, s>>>(a, w.s, z.cols, g.dS_T, g.dS0);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
         if (z.nseg > 0) {
             e = a.io_dtype == FALCON_BF16 ? scan_bwd_io<__nv_bfloat16>(a, g, w, z.ngrp, s) : scan_bwd_io<float>(a, g, w, z.ngrp, s);
             if (e != cudaSuccess) return e;
@@ -656,6 +693,7 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
             }
         }
     }
+    if (single) return cudaSuccess;
     const long long hrows = (long long)a.H * a.dv, hplane = hrows * a.dk;
     const SumJob jobs[3] = {{w.dA, hplane, hplane, g.dA}, {w.dd, hrows, hrows, g.dD}, {w.db, hrows, hrows, g.ddelta_bias}};
     return launch_column_sums(jobs, 3, (long long)z.nwalk * a.B, s);

@@ -453,6 +453,11 @@ def _token_major(B, H, T, d, dev):
     return torch.empty_strided((B, H, T, d), (T * H * d, d, H * d, 1), dtype=torch.float32, device=dev)
 
 
+def _token_majors(n, B, H, T, d, dev):
+    """n of them, made together."""
+    return torch.empty_strided((n, B, H, T, d), (B * T * H * d, T * H * d, d, H * d, 1), dtype=torch.float32, device=dev).unbind()
+
+
 def _workspace(workspace, need, dev):
     """(tensor, address, bytes) of the caller's workspace or of one made here."""
     if workspace is None:
@@ -611,9 +616,9 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
     dev, f32 = v.device, torch.float32
     ctx, raw = _on(dev, stream)
     with ctx:
-        rows = lambda d: _token_major(B, H, T, d, dev)
-        out = {"dq": rows(dk), "dk": rows(dk), "dv": rows(dv), "ddelta": rows(dv),
-               "dz": rows(dv) if z is not None else None,
+        dq, dk_ = _token_majors(2, B, H, T, dk, dev)
+        wide = _token_majors(2 if z is None else 3, B, H, T, dv, dev)
+        out = {"dq": dq, "dk": dk_, "dv": wide[0], "ddelta": wide[1], "dz": None if z is None else wide[2],
                "dA": _dense((H, dv, dk), f32, dev),
                "dD": _dense((H, dv), f32, dev) if D is not None else None,
                "ddelta_bias": _dense((H, dv), f32, dev) if delta_bias is not None else None,
