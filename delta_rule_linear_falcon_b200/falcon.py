@@ -453,6 +453,11 @@ def _token_major(B, H, T, d, dev):
     return torch.empty_strided((B, H, T, d), (T * H * d, d, H * d, 1), dtype=torch.float32, device=dev)
 
 
+def _rows(t, T, H, d):
+    """falcon_view_t of what _token_major made (all zeros for None)."""
+    return _NO_VIEW if t is None else (t.data_ptr(), T * H * d, d, H * d)
+
+
 def _token_majors(n, B, H, T, d, dev):
     """n of them, made together."""
     return torch.empty_strided((n, B, H, T, d), (B * T * H * d, T * H * d, d, H * d, 1), dtype=torch.float32, device=dev).unbind()
@@ -534,12 +539,15 @@ def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None
     with ctx:
         if dx is None:
             dx = _token_major(B, H, T, d, dev)
+            to = _rows(dx, T, H, d)
+        else:
+            to = _seq(dx, "dx", shape, f32, dev)
         out = {"dx": dx, "dw": _dense((H, d, K), f32, dev),
                "dbias": _dense((H, d), f32, dev) if bias is not None else None,
                "dstate": _dense(tail, f32, dev) if state is not None else None}
         a = _conv_args(x, w, bias, act, state, lengths, shape, tail, None, None)
         g = _CONV_GRADS.pack(*_seq(dy, "dy", shape, f32, dev), _arr(dstate_out, "dstate_out", tail, f32, dev),
-                             *_seq(dx, "dx", shape, f32, dev), _at(out["dw"]), _at(out["dbias"]), _at(out["dstate"]))
+                             *to, _at(out["dw"]), _at(out["dbias"]), _at(out["dstate"]))
         need = int((_lib or lib()).falcon_conv_bwd_workspace_size(a))
         workspace, p, n = _workspace(workspace, need, dev)
         _call("falcon_conv_bwd", a, g, p, n, raw)
@@ -624,9 +632,9 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
                "ddelta_bias": _dense((H, dv), f32, dev) if delta_bias is not None else None,
                "dS0": _dense((B, H, dv, dk), f32, dev) if S0 is not None else None}
         a = _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, None, None)
-        views = [x for n, s in (("dq", ks), ("dk", ks), ("dv", vs), ("ddelta", vs), ("dz", vs)) for x in _seq(out[n], n, s, f32, dev)]
-        g = _SCAN_GRADS.pack(*_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev), *views,
-                             _at(out["dA"]), _at(out["dD"]), _at(out["ddelta_bias"]), _at(out["dS0"]))
+        g = _SCAN_GRADS.pack(*_seq(dO, "dO", vs, f32, dev), _arr(dS_T, "dS_T", (B, H, dv, dk), f32, dev),
+                             *_rows(dq, T, H, dk), *_rows(dk_, T, H, dk), *_rows(wide[0], T, H, dv),
+                             *_rows(wide[1], T, H, dv), *_rows(out["dz"], T, H, dv), _at(out["dA"]), _at(out["dD"]), _at(out["ddelta_bias"]), _at(out["dS0"]))
         need = int((_lib or lib()).falcon_scan_bwd_workspace_size(a))
         workspace, p, n = _workspace(workspace, need, dev)
         _call("falcon_scan_bwd", a, g, p, n, raw)
@@ -689,7 +697,7 @@ def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps
                "dwk": _dense(qs[3:], f32, dev) if wk is not None else None}
         a = _qknorm_args(x, qs, ks, q, k, None, None, wq, wk, norm, eps, rot, layout, freq, positions, lengths)
         g = _QKNORM_GRADS.pack(*_seq(dq_out, "dq_out", qs, f32, dev), *_seq(dk_out, "dk_out", ks, f32, dev),
-                               *_seq(out["dq"], "dq", qs, f32, dev), *_seq(out["dk"], "dk", ks, f32, dev),
+                               *_rows(out["dq"], qs[2], qs[1], qs[3]), *_rows(out["dk"], ks[2], ks[1], ks[3]),
                                _at(out["dwq"]), _at(out["dwk"]))
         need = int((_lib or lib()).falcon_qknorm_bwd_workspace_size(a)) if wq is not None or wk is not None else 0
         workspace, p, n = _workspace(workspace, need, dev)
