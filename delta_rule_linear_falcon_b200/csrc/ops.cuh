@@ -65,22 +65,6 @@ template <> struct Pack<__nv_bfloat16, 4> {
         *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
     }
 };
-template <> struct Pack<__nv_bfloat16, 8> {
-    typedef uint4 raw;
-    static __device__ __forceinline__ raw ld(const __nv_bfloat16 *p) { return *reinterpret_cast<const uint4 *>(p); }
-    static __device__ __forceinline__ raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
-    static __device__ __forceinline__ void cvt(raw r, float (&x)[8]) {
-        unpack_bf16x2(r.x, x[0], x[1]);
-        unpack_bf16x2(r.y, x[2], x[3]);
-        unpack_bf16x2(r.z, x[4], x[5]);
-        unpack_bf16x2(r.w, x[6], x[7]);
-    }
-    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[8]) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                   pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    }
-};
-
 // Asynchronous copy of 4, 8 or 16 bytes into the thread's own place in shared memory, and the wait for all but the
 // newest N groups of them.
 template <int BYTES>
@@ -107,12 +91,7 @@ __device__ __forceinline__ float fast_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
 __device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
-__device__ __forceinline__ float silu_grad(float x) {
-    const float g = sigmoid(x);
-    return g * (1.f + x * (1.f - g));
-}
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1, and log(1 + e) / e on [0, 1] by a polynomial whose constant is
 // 1 and whose other eight coefficients are a least-squares fit reweighted towards equal errors (3e-8 of the value, 2e-7
 // with its roundings). As exact for very negative x, where the result is e^x, as for others; one operation of the
