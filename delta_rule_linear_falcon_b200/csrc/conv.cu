@@ -15,7 +15,7 @@
 // dp_t x to dw, and emits dx_{t-K+1} = sum_j w_j dp_{t-j}. The walk goes K - 1 tokens past the run
 // (dp there is formed again by the next run). dw and dbias: registers, then the block's shared memory,
 // then one row of partial sums for each block, summed in a fixed order by a second launch. B4 H16 T4096 d128 bf16:
-// 71 us and 5 us of kernels for 336 MB (51 us at the copy rate), 144 us in all off alignment.
+// 71 us and 5 us of kernels for 336 MB (51 us at the copy rate), 139 us in all off alignment.
 #include "ops.cuh"
 
 namespace falcon {

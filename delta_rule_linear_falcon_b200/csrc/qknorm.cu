@@ -2,18 +2,19 @@
 // the rotation by position in the same pass.
 //
 // A row is read once and written once for a few flops an element: bound by HBM. A row of d channels
-// belongs to LANES neighbouring lanes with NV packs of V channels each (16 bytes of the io type), so a warp
+// belongs to LANES neighbouring lanes with NV packs of V channels each (16 bytes, or 8 of bf16), so a warp
 // moves whole rows; the sum of squares comes from shuffles. Both channels of a rotated pair are in one lane: a
 // pack of FALCON_ROT_HALF is V / 2 channels of the lower half and the V / 2 that turn with them (two 8-byte
 // accesses; exchanging packs between lanes took a shuffle for every channel: 98 us instead of 94 for B8 H16+16
-// T4096 d128 in bf16; with the weights folded into the rotation and two channels an instruction it is 90, 5.9 TB/s). A group of LANES lanes takes one token and walks its heads, kRows of them in flight: the
+// T4096 d128 in bf16; with the weights folded into the rotation and two channels an instruction it is 90, 6 TB/s).
+// A group of LANES lanes takes one token and walks its heads, kRows of them in flight: the
 // token's sines and cosines, the same for every head, are formed once by the block (the angle's whole turns
 // taken off in fp64), kept in registers over the walk, and the row addresses advance by one addition.
 // Where pointers, strides, d or rot are not multiples of a pack, V = 1: lane l owns channels l, l + 32, ..
-// and partners come through shared memory (the same case with rows off alignment: 255 us against 98).
+// and partners come through shared memory (the same case with rows off alignment: 182 us in all against 97).
 // Backward: the same walk with the row turned back; dwq and dwk are summed per lane over the tokens of a
-// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 47 us and 6 us of kernels for 210 MB (32 us at the copy rate);
-// bound by instruction latency, 16 warps an SM (the registers of two rows and their prefetch).
+// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 46 us and 6 us of kernels for
+// 210 MB (32 us at the copy rate), 81 us in all off alignment; bound by instruction latency, 16 warps an SM (the registers of two rows and their prefetch).
 #include "ops.cuh"
 
 namespace falcon {
@@ -51,8 +52,8 @@ __host__ __device__ inline int turn_slots(const falcon_qknorm_args_t &a, int V) 
 }
 
 // (cos, sin) of t quarter turns: whole ones are taken off in fp64, and the rest f, |f| <= 1/2, goes into polynomials in
-// f^2 for sin(f pi/2) / f and cos(f pi/2) (least-squares fits on [0, 1/4], good to 3e-9). With few heads a token's
-// angles are a fifth of its work, and the library's sine and cosine took twice the instructions.
+// f^2 for sin(f pi/2) / f and cos(f pi/2) (least-squares fits on [0, 1/4], good to 3e-9). The library's sine and
+// cosine in its place: 34.4 us against 32.8 for a case of 5 heads with d 256, whose angles few rows share.
 __device__ __forceinline__ float2 turned(double t) {
     const double whole = rint(t);
     const float f = (float)(t - whole), u = f * f;
@@ -536,7 +537,8 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
 }
 
 // The pack's width: 16 bytes of the io type where every row and the rotation allow it (accesses are of half a pack), for
-// bf16 also 8; else one channel.
+// bf16 also 8; else one channel (d 28, all of it rotated, backward: 34 us in packs of 8 bytes, 159 in single channels;
+// d 64 with 6 rotated, forward: 33 us against 58).
 int norm_pack(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g) {
     const int es = a.io_dtype == FALCON_BF16 ? 2 : 4;
     for (int V = 16 / es; V >= 4; V /= 2) {

@@ -11,7 +11,7 @@
 // as 16-byte asynchronous copies into a ring in shared memory, one copy a thread and tensor, and are read there at
 // fixed offsets; o goes back the same way, in the place of z (or v) (loads and stores of single elements, with
 // their addresses, took a fifth of the pass). Where rows are not 16-byte multiples, elements are copied one by one
-// (B1 T16384 dv2048 off alignment: 511 us where this took 370).
+// (B1 T16384 dv2048 off alignment: 503 us against 352).
 // q_t and k_t, the same for all channels of a head, are staged in fp32 and read as broadcasts. Step sizes (softplus)
 // are computed two tokens an instruction, once per channel and token.
 //
