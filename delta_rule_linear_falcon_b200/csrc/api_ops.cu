@@ -252,7 +252,7 @@ falcon_status_t falcon_scan_step(const falcon_scan_args_t *a, falcon_stream_t st
     FALCON_NEED(a->S0 && a->S_out);
     int sms = 0;
     FALCON_TRY(device(&sms));
-    return status_of(launch_scan_step(*a, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(launch_scan_step(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t falcon_scan_bwd_workspace_size(const falcon_scan_args_t *a) {

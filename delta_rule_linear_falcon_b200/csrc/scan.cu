@@ -369,51 +369,75 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
 }
 
 // One token. A channel's row of the state is read and written by G lanes, four columns each, so the state
-// moves in whole lines; each thread has the rows of kStepRows channels in flight, and those of the next sequence
-// while it works on this one's. A block takes the same channels of several sequences: A, as large as a sequence's
-// state, is read once for them (256 sequences, H32 dv128 dk16: 35 us for each launch alone with eight, 41 with one; 4.9
-// TB/s among others). A channel's scalars (step, dt v, output) belong to one of its lanes.
-constexpr int kStepThreads = 128, kStepRows = 4;
+// moves in whole lines. A thread has the rows of kStepRows channels and works through several sequences: A, as large
+// as a sequence's state, is read once for them, and the states come through a ring of asynchronous copies into places
+// that only the copying thread reads (no barrier; bytes in flight cost no registers). A channel's scalars (step, dt v,
+// output) belong to one of its lanes and are loaded one sequence ahead. HBM bounds it: bf16, dk = 16, 256 sequences of
+// H32 dv128 28 us, 5.2 TB/s; 1024 of H32 dv64 dk64 173 us, 6.2 TB/s (38 and 260 us with the next sequence's rows in
+// registers, which left five blocks an SM). Blocks an SM and places of the ring, for these two: six and three 28 and 173
+// us, eight and three (64 registers) 30 and 180, six and four 29 and 173, ten and two 32 and 198. dk = 15, whose rows
+// are not 16-byte aligned and go by four bytes: 40 us against the 28.
+constexpr int kStepThreads = 128, kStepRows = 4, kStepRing = 3, kStepBlocks = 6;
 
 template <typename IO, int G, bool V4>
-__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_args_t a, int ngrp, int chunk) {
+__global__ void __launch_bounds__(kStepThreads, kStepBlocks) scan_step_kernel(falcon_scan_args_t a, int ngrp, int chunk) {
     constexpr int CPP = kStepThreads / G;                          // channels of a pass
     constexpr int OWN = G >= kStepRows ? 1 : kStepRows / G;        // rows whose scalars this lane keeps
+    typedef Pack<IO, V4 ? 4 : 1> P;
+    constexpr int NK = V4 ? 1 : 4;
+    __shared__ __align__(16) float ring[kStepRing][kStepRows][kStepThreads][4];
     const int grp = blockIdx.x % (unsigned)ngrp;
     const unsigned rest = blockIdx.x / (unsigned)ngrp;
     const int h = rest % (unsigned)a.H;
     const int b0 = (int)(rest / (unsigned)a.H) * chunk, b1 = min(b0 + chunk, a.B);
-    const int lane = threadIdx.x & 31, sl = threadIdx.x % G, c0 = sl * 4;
-    const int ch0 = grp * CPP * kStepRows + threadIdx.x / G;
-    const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0, cols = c0 < a.dk;
+    const int tid = threadIdx.x, lane = tid & 31, sl = tid % G, c0 = sl * 4;
+    const int ch0 = grp * CPP * kStepRows + tid / G;
+    const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0;
     // the row whose total lanes_sum leaves in this lane, and the lane of the group that keeps row i
     const int own = G >= kStepRows ? sl / (G / kStepRows > 0 ? G / kStepRows : 1) : sl * OWN;
     const bool writes = G < kStepRows || sl % (G / kStepRows > 0 ? G / kStepRows : 1) == 0;
     auto keeper = [](int i) { return G >= kStepRows ? i * (G / kStepRows) : i / OWN; };
+    // element r of row i is one of the state's (V4: all four or none)
+    auto there = [&](int i, int r) { return ch0 + i * CPP < a.dv && c0 + (V4 ? 0 : r) < a.dk; };
 
-    auto row4 = [&](const float *p, float (&x)[4]) {
-        if (V4) {
-            const float4 f = __ldcs(reinterpret_cast<const float4 *>(p + c0));
-            x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-        } else {
+    // ---- the states: this thread's part of sequence b, `per` elements from one sequence's to the next
+    const long long per = (long long)a.H * a.dv * a.dk, first = ((long long)b0 * a.H + h) * a.dv * a.dk + (long long)ch0 * a.dk + c0;
+    const float *from = a.S0 + first;
+    float *to = a.S_out + first;
+    auto ask = [&](int place, bool any) {
+        if (any) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = c0 + r < a.dk ? __ldcs(p + c0 + r) : 0.f;
+            for (int i = 0; i < kStepRows; ++i) {
+                if (V4) {
+                    if (there(i, 0)) copy_async<16>(ring[place][i][tid], from + i * CPP * a.dk);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (there(i, r)) copy_async<4>(&ring[place][i][tid][r], from + i * CPP * a.dk + r);
+                }
+            }
         }
+        from += per;
+        copy_commit();
     };
-    float S[kStepRows][4], A2[kStepRows][4], q[4], k[4], raw[OWN], v[OWN], z[OWN], bias[OWN], skip[OWN];
+#pragma unroll
+    for (int j = 0; j < kStepRing - 1; ++j) ask(j, b0 + j < b1);
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (!there(i, r))
+#pragma unroll
+                for (int j = 0; j < kStepRing; ++j) ring[j][i][tid][r] = 0.f;
+
+    typename P::raw rq[NK], rk[NK];
+    float raw[OWN], v[OWN], z[OWN], bias[OWN], skip[OWN];
     auto fetch = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < kStepRows; ++i) {
-            const int ch = ch0 + i * CPP;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[i][r] = 0.f;
-            if (ch < a.dv && cols) row4(a.S0 + (((long long)b * a.H + h) * a.dv + ch) * a.dk, S[i]);
-        }
         const IO *pq = row_of<IO>(a.q, b, h, 0), *pk = row_of<IO>(a.k, b, h, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            q[r] = c0 + r < a.dk ? Io<IO>::ld(pq, c0 + r) : 0.f;
-            k[r] = c0 + r < a.dk ? Io<IO>::ld(pk, c0 + r) : 0.f;
+        for (int r = 0; r < NK; ++r) {
+            rq[r] = c0 + r < a.dk ? P::ld(pq + c0 + r) : P::zero();
+            rk[r] = c0 + r < a.dk ? P::ld(pk + c0 + r) : P::zero();
         }
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
@@ -426,23 +450,36 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_arg
             }
         }
     };
-    fetch(b0);
+    auto columns = [&](const typename P::raw (&x)[NK], f32x2 (&to2)[2]) {
+        float f[4];
+        if constexpr (V4) {
+            P::cvt(x[0], f);
+        } else {
 #pragma unroll
-    for (int i = 0; i < kStepRows; ++i) {
-        const int ch = ch0 + i * CPP;
-        const float *row = a.A + ((long long)h * a.dv + ch) * a.dk + c0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) A2[i][r] = 0.f;
-        if (ch < a.dv && cols) {
-            if (V4) {
-                const float4 f = *reinterpret_cast<const float4 *>(row);
-                A2[i][0] = f.x * kLog2e; A2[i][1] = f.y * kLog2e; A2[i][2] = f.z * kLog2e; A2[i][3] = f.w * kLog2e;
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (c0 + r < a.dk) A2[i][r] = row[r] * kLog2e;
+            for (int r = 0; r < 4; ++r) {
+                float one[1];
+                P::cvt(x[r], one);
+                f[r] = one[0];
             }
         }
+        to2[0] = pack2(f[0], f[1]);
+        to2[1] = pack2(f[2], f[3]);
+    };
+    fetch(b0);
+    f32x2 A2[kStepRows][2];
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i) {
+        const float *row = a.A + ((long long)h * a.dv + ch0 + i * CPP) * a.dk + c0;
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (V4) {
+            if (there(i, 0)) Pack<float, 4>::cvt(Pack<float, 4>::ld(row), f);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (there(i, r)) f[r] = row[r];
+        }
+        A2[i][0] = pack2(f[0] * kLog2e, f[1] * kLog2e);
+        A2[i][1] = pack2(f[2] * kLog2e, f[3] * kLog2e);
     }
 #pragma unroll
     for (int j = 0; j < OWN; ++j) {
@@ -450,9 +487,11 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_arg
         bias[j] = ch < a.dv && a.delta_bias ? a.delta_bias[(long long)h * a.dv + ch] : 0.f;
         skip[j] = ch < a.dv && a.D ? a.D[(long long)h * a.dv + ch] : 0.f;
     }
+    int place = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-        float dt[OWN], dtv[OWN], vv[OWN], zz[OWN], y[kStepRows], T[kStepRows][4];
+        float dt[OWN], dtv[OWN], vv[OWN], zz[OWN], y[kStepRows];
+        f32x2 q[2], k[2];
 #pragma unroll
         for (int j = 0; j < OWN; ++j) {
             const float x = raw[j] + bias[j];
@@ -461,32 +500,36 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(falcon_scan_arg
             vv[j] = v[j];
             zz[j] = z[j];
         }
+        columns(rq, q);
+        columns(rk, k);
+        if (b + 1 < b1) fetch(b + 1);
+        // the place that is filled now was read a sequence ago
+        ask(place == 0 ? kStepRing - 1 : place - 1, b + kStepRing - 1 < b1);
+        copy_wait<kStepRing - 1>();
 #pragma unroll
         for (int i = 0; i < kStepRows; ++i) {
             const float d = __shfl_sync(0xffffffffu, dt[i % OWN], keeper(i), G), x = __shfl_sync(0xffffffffu, dtv[i % OWN], keeper(i), G);
-            y[i] = 0.f;
+            const f32x2 d2 = pack2(d, d), x2 = pack2(x, x);
+            f32x2 S[2];
+            load_pairs(ring[place][i][tid], S[0], S[1]);
+            S[0] = fma2(ex2_2(mul2(d2, A2[i][0])), S[0], mul2(x2, k[0]));
+            S[1] = fma2(ex2_2(mul2(d2, A2[i][1])), S[1], mul2(x2, k[1]));
+            y[i] = sum2(fma2(S[1], q[1], mul2(S[0], q[0])));
+            float f[4];
+            unpack2(S[0], f[0], f[1]);
+            unpack2(S[1], f[2], f[3]);
+            if (V4) {
+                if (there(i, 0)) __stcs(reinterpret_cast<float4 *>(to + i * CPP * a.dk), make_float4(f[0], f[1], f[2], f[3]));
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                T[i][r] = fmaf(fast_ex2(d * A2[i][r]), S[i][r], x * k[r]);
-                y[i] = fmaf(T[i][r], q[r], y[i]);
+                for (int r = 0; r < 4; ++r)
+                    if (there(i, r)) __stcs(to + i * CPP * a.dk + r, f[r]);
             }
         }
-        if (b + 1 < b1) fetch(b + 1);
-        const long long bh = (long long)b * a.H + h;
-#pragma unroll
-        for (int i = 0; i < kStepRows; ++i) {
-            const int ch = ch0 + i * CPP;
-            if (ch < a.dv && cols) {
-                float *to = a.S_out + (bh * a.dv + ch) * a.dk + c0;
-                if (V4) __stcs(reinterpret_cast<float4 *>(to), make_float4(T[i][0], T[i][1], T[i][2], T[i][3]));
-                else
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (c0 + r < a.dk) __stcs(to + r, T[i][r]);
-            }
-        }
-        bool first;
-        lanes_sum<kStepRows, G, 1>(y, lane, first);
+        to += per;
+        place = place + 1 == kStepRing ? 0 : place + 1;
+        bool alone;
+        lanes_sum<kStepRows, G, 1>(y, lane, alone);
         if (writes) {
             IO *po = row_of<IO>(a.o, b, h, 0);
 #pragma unroll
@@ -534,27 +577,39 @@ cudaError_t scan_pass_io(int mode, const falcon_scan_args_t &a, const ScanWork &
 }
 
 template <typename IO, int G>
-cudaError_t scan_step_t(const falcon_scan_args_t &a, cudaStream_t s) {
+cudaError_t scan_step_t(const falcon_scan_args_t &a, int num_sms, cudaStream_t s) {
     const int per = kStepThreads / G * kStepRows;
     const int ngrp = (a.dv + per - 1) / per;
-    int chunk = 8;   // sequences of a block, while two blocks a place on the GPU are left
-    while (chunk > 1 && (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk) < 148 * 8) chunk /= 2;
-    const long long blocks = (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk);
+    // sequences of a block: the number with the shortest estimate, in turns of the blocks that the SMs hold at once
+    // (a block's start, with its rows of A, costs about one sequence). 256 sequences of H32 dv128: 10 to a block and
+    // one turn 28 us; 8 and 1.2 turns 34, 4 and 2.3 turns 31, one and 9.2 turns 38.
+    auto blocks_of = [&](int chunk) { return (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk); };
+    int chunk = 1;
+    long long best = 0;
+    for (int c = 1; c <= 32 && c <= a.B; ++c) {
+        const long long cost = (blocks_of(c) + num_sms * kStepBlocks - 1) / (num_sms * kStepBlocks) * (c + 1);
+        if (c == 1 || cost < best) {
+            best = cost;
+            chunk = c;
+        }
+    }
+    const long long blocks = blocks_of(chunk);
     if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const uintptr_t any = reinterpret_cast<uintptr_t>(a.S0) | reinterpret_cast<uintptr_t>(a.S_out) | reinterpret_cast<uintptr_t>(a.A);
-    if (a.dk % 4 == 0 && any % 16 == 0) scan_step_kernel<IO, G, true><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp, chunk);
+    const bool v4 = a.dk % 4 == 0 && any % 16 == 0 && view_packs(a.q, 4, sizeof(IO)) && view_packs(a.k, 4, sizeof(IO));
+    if (v4) scan_step_kernel<IO, G, true><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp, chunk);
     else scan_step_kernel<IO, G, false><<<(unsigned)blocks, kStepThreads, 0, s>>>(a, ngrp, chunk);
     return cudaGetLastError();
 }
 
 template <typename IO>
-cudaError_t scan_step_io(const falcon_scan_args_t &a, cudaStream_t s) {
-    if (a.dk <= 4) return scan_step_t<IO, 1>(a, s);
-    if (a.dk <= 8) return scan_step_t<IO, 2>(a, s);
-    if (a.dk <= 16) return scan_step_t<IO, 4>(a, s);
-    if (a.dk <= 32) return scan_step_t<IO, 8>(a, s);
-    if (a.dk <= 64) return scan_step_t<IO, 16>(a, s);
-    return scan_step_t<IO, 32>(a, s);
+cudaError_t scan_step_io(const falcon_scan_args_t &a, int num_sms, cudaStream_t s) {
+    if (a.dk <= 4) return scan_step_t<IO, 1>(a, num_sms, s);
+    if (a.dk <= 8) return scan_step_t<IO, 2>(a, num_sms, s);
+    if (a.dk <= 16) return scan_step_t<IO, 4>(a, num_sms, s);
+    if (a.dk <= 32) return scan_step_t<IO, 8>(a, num_sms, s);
+    if (a.dk <= 64) return scan_step_t<IO, 16>(a, num_sms, s);
+    return scan_step_t<IO, 32>(a, num_sms, s);
 }
 
 }  // namespace
@@ -614,9 +669,9 @@ cudaError_t launch_scan_fwd(const falcon_scan_args_t &a, const ScanPlan &plan, f
     return launch_scan_pass(kScanFull, a, w, s);
 }
 
-cudaError_t launch_scan_step(const falcon_scan_args_t &a, cudaStream_t s) {
+cudaError_t launch_scan_step(const falcon_scan_args_t &a, int num_sms, cudaStream_t s) {
     if ((long long)a.B * a.H == 0) return cudaSuccess;
-    return a.io_dtype == FALCON_BF16 ? scan_step_io<__nv_bfloat16>(a, s) : scan_step_io<float>(a, s);
+    return a.io_dtype == FALCON_BF16 ? scan_step_io<__nv_bfloat16>(a, num_sms, s) : scan_step_io<float>(a, num_sms, s);
 }
 
 }  // namespace falcon
