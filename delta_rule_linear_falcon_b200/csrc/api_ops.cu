@@ -198,7 +198,7 @@ falcon_status_t falcon_conv_step(const falcon_conv_args_t *a, falcon_stream_t st
     FALCON_NEED(a->K == 1 || (a->state && a->state_out));
     int sms = 0;
     FALCON_TRY(device(&sms));
-    return status_of(launch_conv_step(*a, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(launch_conv_step(*a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t falcon_conv_bwd_workspace_size(const falcon_conv_args_t *a) {

@@ -22,7 +22,7 @@ cudaError_t launch_column_sums(const SumJob *jobs, int njobs, long long nparts, 
 
 // convolution (conv.cu)
 cudaError_t launch_conv_fwd(const falcon_conv_args_t &a, int num_sms, cudaStream_t s);
-cudaError_t launch_conv_step(const falcon_conv_args_t &a, cudaStream_t s);
+cudaError_t launch_conv_step(const falcon_conv_args_t &a, int num_sms, cudaStream_t s);
 size_t conv_bwd_workspace(const falcon_conv_args_t &a);
 cudaError_t launch_conv_bwd(const falcon_conv_args_t &a, const falcon_conv_grads_t &g, float *ws, cudaStream_t s);
 

@@ -154,3 +154,43 @@ def test_qknorm_backward_in_place(F):
     grads = F.FalconQknormGrads(dq_out=view(gq), dq=view(gq))
     assert F.lib().falcon_qknorm_bwd(ctypes.byref(a), ctypes.byref(grads), None, 0, torch.cuda.current_stream().cuda_stream) == F.FALCON_OK
     assert torch.equal(gq, want)
+
+
+# Many sequences: a block or thread works through several of them, the last one through fewer. Each sequence is what a
+# call on a few of them gives, to the last bit.
+
+FEW = [slice(0, 5), slice(300, 307), slice(-4, None)]
+
+
+@pytest.mark.parametrize("io,N,H,d,K", [("bf16", 601, 16, 128, 4), ("bf16", 405, 12, 200, 8), ("bf16", 601, 8, 33, 3), ("f32", 601, 16, 128, 4),
+                                        ("f32", 405, 16, 101, 6)])
+def test_conv_step_of_many_sequences(F, io, N, H, d, K):
+    r = torch.Generator(device="cuda").manual_seed(40)
+    rand = lambda *s: torch.randn(*s, generator=r, device="cuda")
+    x, state = rand(N, H, d).to(IO[io]), rand(N, H, K - 1, d).to(IO[io])
+    w, bias = rand(H, d, K), rand(H, d)
+    out = torch.empty_like(state)
+    y = F.falcon_conv_step(x, w, state, bias=bias, state_out=out)
+    for few in FEW:
+        part = state[few].clone()
+        want = F.falcon_conv_step(x[few], w, part, bias=bias)
+        assert torch.equal(y[few], want) and torch.equal(out[few], part)
+    assert torch.equal(out[:, :, -1], x) and torch.equal(out[:, :, :-1], state[:, :, 1:])
+    assert torch.equal(F.falcon_conv_step(x, w, state, bias=bias), y) and torch.equal(state, out)
+
+
+@pytest.mark.parametrize("io,N,H,dk,dv", [("bf16", 901, 8, 16, 128), ("f32", 901, 8, 16, 128), ("bf16", 907, 4, 64, 64), ("f32", 701, 8, 15, 100),
+                                          ("bf16", 601, 8, 128, 32), ("f32", 2003, 8, 3, 130)])
+def test_scan_step_of_many_sequences(F, io, N, H, dk, dv):
+    r = torch.Generator(device="cuda").manual_seed(41)
+    rand = lambda *s: torch.randn(*s, generator=r, device="cuda")
+    seq = {n: rand(N, H, dk if n in "qk" else dv).to(IO[io]) for n in ("q", "k", "v", "delta", "z")}
+    par = {"A": -rand(H, dv, dk).exp(), "D": rand(H, dv), "delta_bias": rand(H, dv)}
+    S = rand(N, H, dv, dk)
+    S_out = torch.empty_like(S)
+    o = F.falcon_scan_step(S=S, S_out=S_out, **seq, **par)
+    for few in FEW:
+        part = S[few].clone()
+        want = F.falcon_scan_step(S=part, **{n: x[few] for n, x in seq.items()}, **par)
+        assert torch.equal(o[few], want) and torch.equal(S_out[few], part)
+    assert torch.equal(F.falcon_scan_step(S=S, **seq, **par), o) and torch.equal(S, S_out)
