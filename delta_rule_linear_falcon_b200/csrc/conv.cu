@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(kStepThreads, step_blocks(K)) conv_step_kernel
     typedef Pack<IO, V> P;
     const long long packs = (long long)a.H * nv;
     const long long g = (long long)blockIdx.x * kStepThreads + threadIdx.x;
-    const int b0 = (int)(g / packs) * chunk, b1 = min(b0 + chunk, a.B);
+    const long long start = g / packs * chunk;   // behind the last sequence in threads that the last block has left over
+    if (start >= a.B) return;
+    const int b0 = (int)start, b1 = b0 + min(chunk, a.B - b0);
     const int pack = (int)(g % packs);
     const int h = pack / nv, c0 = (pack % nv) * V;
-    if (b0 >= b1) return;
     typename P::raw next[K];   // the tail, then the token
     auto fetch = [&](int b) {
 #pragma unroll
@@ -529,7 +530,7 @@ cudaError_t conv_step_io(const falcon_conv_args_t &a, int num_sms, cudaStream_t 
     // sequences of a thread: the number with the shortest estimate, in turns of the threads that the SMs hold at once
     // (a thread's start, with its weights, costs about one sequence). For fp32, whose weights weigh half as much, up to two:
     // 4096 sequences of H32 d128 K4 take 87 us with two, 90 with seven, 93 with one.
-    auto all = [&](int chunk) { return packs * ((a.B + chunk - 1) / chunk); };
+    auto all = [&](int chunk) { return packs * ((a.B - 1LL + chunk) / chunk); };
     int chunk = 1;
     long long best = 0;
     for (int c = 1; c <= (sizeof(IO) == 2 ? 32 : 2) && c <= a.B; ++c) {

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) scan_step_kernel(fa
     const int grp = blockIdx.x % (unsigned)ngrp;
     const unsigned rest = blockIdx.x / (unsigned)ngrp;
     const int h = rest % (unsigned)a.H;
-    const int b0 = (int)(rest / (unsigned)a.H) * chunk, b1 = min(b0 + chunk, a.B);
+    const int b0 = (int)(rest / (unsigned)a.H) * chunk, b1 = b0 + min(chunk, a.B - b0);
     const int tid = threadIdx.x, lane = tid & 31, sl = tid % G, c0 = sl * 4;
     const int ch0 = grp * CPP * kStepRows + tid / G;
     const bool soft = (a.flags & FALCON_SCAN_SOFTPLUS) != 0;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) scan_step_kernel(fa
         copy_commit();
     };
 #pragma unroll
-    for (int j = 0; j < kStepRing - 1; ++j) ask(j, b0 + j < b1);
+    for (int j = 0; j < kStepRing - 1; ++j) ask(j, j < b1 - b0);
 #pragma unroll
     for (int i = 0; i < kStepRows; ++i)
 #pragma unroll
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) scan_step_kernel(fa
         columns(rk, k);
         if (b + 1 < b1) fetch(b + 1);
         // the place that is filled now was read a sequence ago
-        ask(place == 0 ? kStepRing - 1 : place - 1, b + kStepRing - 1 < b1);
+        ask(place == 0 ? kStepRing - 1 : place - 1, b1 - b > kStepRing - 1);
         copy_wait<kStepRing - 1>();
 #pragma unroll
         for (int i = 0; i < kStepRows; ++i) {
@@ -583,7 +583,7 @@ cudaError_t scan_step_t(const falcon_scan_args_t &a, int num_sms, cudaStream_t s
     // sequences of a block: the number with the shortest estimate, in turns of the blocks that the SMs hold at once
     // (a block's start, with its rows of A, costs about one sequence). 256 sequences of H32 dv128: 10 to a block and
     // one turn 28 us; 8 and 1.2 turns 34, 4 and 2.3 turns 31, one and 9.2 turns 38.
-    auto blocks_of = [&](int chunk) { return (long long)ngrp * a.H * ((a.B + chunk - 1) / chunk); };
+    auto blocks_of = [&](int chunk) { return (long long)ngrp * a.H * ((a.B - 1LL + chunk) / chunk); };
     int chunk = 1;
     long long best = 0;
     for (int c = 1; c <= 32 && c <= a.B; ++c) {

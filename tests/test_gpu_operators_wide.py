@@ -194,3 +194,11 @@ def test_scan_step_of_many_sequences(F, io, N, H, dk, dv):
         want = F.falcon_scan_step(S=part, **{n: x[few] for n, x in seq.items()}, **par)
         assert torch.equal(o[few], want) and torch.equal(S_out[few], part)
     assert torch.equal(F.falcon_scan_step(S=S, **seq, **par), o) and torch.equal(S, S_out)
+
+
+def test_conv_step_of_the_most_sequences(F):
+    """2^31 - 1 rows of one channel: sequence numbers behind the last one pass 31 bits in the last block."""
+    N = 2 ** 31 - 1
+    x = torch.arange(N, dtype=torch.int32, device="cuda").remainder_(251).to(torch.bfloat16).view(N, 1, 1)
+    y = F.falcon_conv_step(x, torch.ones(1, 1, 1, device="cuda"), torch.empty(N, 1, 0, 1, dtype=torch.bfloat16, device="cuda"), act="none")
+    assert torch.equal(y, x)
