@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kScanThreads, MODE == kScanBoth ? 3 : 4) scan_
     auto column = [&](const float *row, int s) { return ok && row && sl * ST + s < a.dk ? row[sl * ST + s] : 0.f; };
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
-        A2[s] = pack2(column(a.A + hc * a.dk, 2 * s) * kLog2e, column(a.A + hc * a.dk, 2 * s + 1) * kLog2e);
+        A2[s] = pack2(decay_rate(column(a.A + hc * a.dk, 2 * s)), decay_rate(column(a.A + hc * a.dk, 2 * s + 1)));
         S[s] = 0ull;
         if (MODE == kScanBoth) { Pr[s] = pack2(1.f, 1.f); G[s] = 0ull; }
     }
@@ -478,8 +478,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocks) scan_step_kernel(fa
             for (int r = 0; r < 4; ++r)
                 if (there(i, r)) f[r] = row[r];
         }
-        A2[i][0] = pack2(f[0] * kLog2e, f[1] * kLog2e);
-        A2[i][1] = pack2(f[2] * kLog2e, f[3] * kLog2e);
+        A2[i][0] = pack2(decay_rate(f[0]), decay_rate(f[1]));
+        A2[i][1] = pack2(decay_rate(f[2]), decay_rate(f[3]));
     }
 #pragma unroll
     for (int j = 0; j < OWN; ++j) {

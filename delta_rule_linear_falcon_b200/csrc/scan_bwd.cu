@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(falcon_scan_args_t a, Sc
     const long long row = e / cols;
     const int c = (int)(e % cols);
     if (row >= rows || c >= a.dk) return;
-    const float A2 = a.A[row % ((long long)a.H * a.dv) * a.dk + c] * kLog2e;
+    const float A2 = decay_rate(a.A[row % ((long long)a.H * a.dv) * a.dk + c]);
     const float *steps = w.wsteps + row * w.nwalk;
     constexpr int U = 16;   // walks in flight
     if (blockIdx.y == 0) {
@@ -146,7 +146,7 @@ scan_bwd_kernel(falcon_scan_args_t a, falcon_scan_grads_t g, ScanBwdWork w, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int ch = c00 + lc + i;
-            x[i] = ch < a.dv && c < a.dk ? a.A[((long long)h * a.dv + ch) * a.dk + c] * kLog2e : 0.f;
+            x[i] = ch < a.dv && c < a.dk ? decay_rate(a.A[((long long)h * a.dv + ch) * a.dk + c]) : 0.f;
         }
         A2[0][s] = pack2(x[0], x[1]);
         A2[1][s] = pack2(x[2], x[3]);

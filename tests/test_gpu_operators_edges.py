@@ -1,0 +1,69 @@
+"""Values and sizes at the edge of what the operators around the memory allow, against the 64-bit forms of
+oracle/operators.py with the bounds of test_gpu_operators.py."""
+import pytest
+import torch
+
+from oracle import operators as O
+from test_gpu_operators import F, IO, close, gradients_close, half_step, scan_bound, scan_inputs  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ scan: entries that forget everything
+
+FORGET = [  # io, B, H, T, dk, dv, order, lengths
+    ("bf16", 2, 2, 21, 16, 64, None, [21, 13]),        # tokens behind the end inside a chunk of eight
+    ("f32", 3, 1, 19, 11, 30, "odd", [19, 0, 1]),
+    ("bf16", 1, 2, 37, 40, 24, "token", None),
+    ("bf16", 2, 1, 900, 16, 40, None, [900, 101]),     # segments without a token behind a ragged end
+    ("f32", 1, 1, 700, 5, 9, None, None),
+]
+
+
+def forgetting(seed, io, B, H, T, dk, dv, order):
+    """Inputs whose A has columns of -inf and of a finite value that overflows times log2 e. The 64-bit form gets -1e30
+    in their place: the same decays, all 0, and a gradient that is no 0 x inf."""
+    h, g, r = scan_inputs(seed, io, B, H, T, dk, dv, True, True, True, True, order)
+    for c, x in ((0, float("-inf")), (2, -3e38)):
+        h["A"][:, :, c], g["A"][:, :, c] = -1e30, x
+    return h, g, r
+
+
+@pytest.mark.parametrize("io,B,H,T,dk,dv,order,lengths", FORGET)
+def test_scan_forgets(F, io, B, H, T, dk, dv, order, lengths):
+    h, g, r = forgetting(50, io, B, H, T, dk, dv, order)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    want, S_w = O.scan(**h, lengths=lengths)
+    bo, bS = scan_bound(h, True, lengths, T)
+    for ws in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):   # split where it pays; never split
+        o, S = F.falcon_scan_fwd(**g, lengths=n, o=torch.zeros(B, H, T, dv, dtype=IO[io], device="cuda"), workspace=ws)
+        close(o, want, bo + half_step(io, want), "o")
+        close(S, S_w, bS, "S")
+    dO, dO_g = r(B, H, T, dv)
+    dS, dS_g = r(B, H, dv, dk)
+    got = F.falcon_scan_bwd(**g, dO=dO_g, lengths=n, dS_T=dS_g)
+    leaves = {k: v.clone().requires_grad_() for k, v in h.items()}
+    outs = O.scan(**{k: leaves.get(k) for k in h}, lengths=lengths)
+    gradients_close(got, {"d" + k: v for k, v in O.gradients(outs, (dO, dS), leaves).items() if k != "delta_bias"}, T)
+
+
+def test_scan_step_forgets(F):
+    h, g, _ = forgetting(51, "f32", 3, 2, 1, 16, 40, None)
+    want, S_w = O.scan(**h)
+    bo, bS = scan_bound(h, True, None, 1)
+    one = {k: (v if k in ("A", "D", "delta_bias", "S0") else v[:, :, 0]) for k, v in g.items()}
+    S = one.pop("S0")
+    close(F.falcon_scan_step(S=S, **one), want[:, :, 0], bo[:, :, 0], "o")
+    close(S, S_w, bS, "S")
+    # a step of 0 keeps the state, whatever A is
+    one.update(delta=torch.zeros_like(one["delta"]), delta_bias=None, softplus=False)
+    kept = S.clone()
+    F.falcon_scan_step(S=S, **one)
+    assert torch.equal(S, kept)
+
+
+def test_scan_nan_in_A_is_seen(F):
+    _, g, _ = scan_inputs(52, "f32", 1, 1, 12, 16, 8, True, False, False, True, None)
+    g["A"][0, 3, 5] = float("nan")
+    _, S = F.falcon_scan_fwd(**g)
+    assert S[0, 0, 3, 5].isnan() and int(S.isnan().sum()) == 1
