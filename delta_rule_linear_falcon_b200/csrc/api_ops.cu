@@ -3,6 +3,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "launch.h"
 #include "ops.h"
 
@@ -57,6 +59,21 @@ falcon_status_t check_view(const falcon_view_t &v, int B, int H, int T, int d, s
     return FALCON_OK;
 }
 
+// Where `rows` rows of a view start, NULL where there is none.
+const void *start(const falcon_view_t &v, long long rows) { return rows > 0 ? v.p : nullptr; }
+
+// No output starts where another one or an input does (what overlaps in another way is not seen here).
+bool apart(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins) {
+    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void *const *p = outs.begin(); p != o; ++p)
+            if (*p == *o) return false;
+        for (const void *i : ins)
+            if (i == *o) return false;
+    }
+    return true;
+}
+
 // Parameters, lengths and states: device arrays of 4-byte elements (or io elements of es bytes).
 bool ok_array(const void *p, bool required, size_t es = 4) { return p ? aligned(p, es) : !required; }
 
@@ -106,6 +123,10 @@ falcon_status_t check_conv_out(const falcon_conv_args_t *a) {
     FALCON_TRY(check_view(a->y, a->B, a->H, a->T, a->d, es, true));
     FALCON_NEED(ok_array(a->state_out, false, es));
     FALCON_NEED(!a->y.p || a->y.p != a->x.p);   // a row is read again after its successors are written
+    const long long rows = (long long)a->B * a->H * a->T, tail = (long long)a->B * a->H * (a->K - 1);
+    const void *const state_out = tail > 0 ? a->state_out : nullptr;
+    FALCON_NEED(apart({start(a->y, rows), state_out}, {start(a->x, rows)}));
+    FALCON_NEED(apart({start(a->y, rows)}, {tail > 0 ? a->state : nullptr}));   // state_out may be state
     return FALCON_OK;
 }
 
@@ -138,6 +159,10 @@ falcon_status_t check_scan_out(const falcon_scan_args_t *a) {
     FALCON_TRY(check_view(a->o, a->B, a->H, a->T, a->dv, elem_size(a->io_dtype), true));
     if (far_tokens(a->o, a->T)) return FALCON_ERR_UNSUPPORTED;
     FALCON_NEED(ok_array(a->S_out, false));
+    const long long rows = (long long)a->B * a->H * a->T;   // other blocks still read q and k of a token that is written
+    FALCON_NEED(apart({start(a->o, rows), a->S_out}, {start(a->q, rows), start(a->k, rows), start(a->v, rows),
+                                                      start(a->delta, rows), start(a->z, rows)}));
+    FALCON_NEED(apart({start(a->o, rows)}, {a->S0}));       // S_out may be S0
     return FALCON_OK;
 }
 
@@ -171,6 +196,10 @@ falcon_status_t check_qknorm_out(const falcon_qknorm_args_t *a) {
     FALCON_TRY(check_view(a->q_out, a->B, a->Hq, a->T, a->d, es, true));
     FALCON_TRY(check_view(a->k_out, a->B, a->Hk, a->T, a->d, es, true));
     FALCON_NEED(same_place(a->q, a->q_out) && same_place(a->k, a->k_out));
+    const long long tokens = (long long)a->B * a->T;
+    const void *const q = start(a->q, tokens * a->Hq), *const k = start(a->k, tokens * a->Hk);
+    const void *const q_out = start(a->q_out, tokens * a->Hq), *const k_out = start(a->k_out, tokens * a->Hk);
+    FALCON_NEED(apart({q_out, k_out}, {}) && apart({q_out}, {k}) && apart({k_out}, {q}));
     return FALCON_OK;
 }
 
@@ -214,6 +243,10 @@ falcon_status_t falcon_conv_bwd(const falcon_conv_args_t *a, const falcon_conv_g
     FALCON_NEED(!g->dx.p || g->dx.p != g->dy.p);
     FALCON_NEED(ok_array(g->dw, a->H > 0) && ok_array(g->dbias, false) && ok_array(g->dstate_out, false) &&
                 ok_array(g->dstate, false));
+    const long long rows = (long long)a->B * a->H * a->T;
+    const bool tail = (long long)a->B * a->H * (a->K - 1) > 0;
+    FALCON_NEED(apart({start(g->dx, rows), g->dw, g->dbias, tail ? g->dstate : nullptr},
+                      {start(a->x, rows), start(g->dy, rows), tail ? a->state : nullptr, tail ? g->dstate_out : nullptr}));
     if (a->H == 0) return FALCON_OK;
     FALCON_TRY(check_workspace(workspace, workspace_bytes, conv_bwd_workspace(*a)));
     int sms = 0;
@@ -275,6 +308,12 @@ falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *a, const falcon_scan_g
     }
     FALCON_NEED(ok_array(g->dS_T, false) && ok_array(g->dA, a->H > 0) && ok_array(g->dD, false) &&
                 ok_array(g->ddelta_bias, false) && ok_array(g->dS0, false));
+    const long long rows = (long long)a->B * a->H * a->T;
+    const void *const dS0 = a->B > 0 ? g->dS0 : nullptr;
+    FALCON_NEED(apart({start(g->dq, rows), start(g->dk, rows), start(g->dv, rows), start(g->ddelta, rows), start(g->dz, rows),
+                       g->dA, g->dD, g->ddelta_bias, dS0},
+                      {start(g->dO, rows), start(a->q, rows), start(a->k, rows), start(a->v, rows), start(a->delta, rows),
+                       start(a->z, rows), a->S0}));
     if (a->H == 0) return FALCON_OK;
     FALCON_TRY(check_workspace(workspace, workspace_bytes, scan_bwd_workspace(*a)));
     int sms = 0;
@@ -304,6 +343,11 @@ falcon_status_t falcon_qknorm_bwd(const falcon_qknorm_args_t *a, const falcon_qk
     FALCON_TRY(check_view(g->dq, a->B, a->Hq, a->T, a->d, 4, true));
     FALCON_TRY(check_view(g->dk, a->B, a->Hk, a->T, a->d, 4, true));
     FALCON_NEED(same_place(g->dq, g->dq_out) && same_place(g->dk, g->dk_out));
+    const long long tokens = (long long)a->B * a->T;
+    const void *const q = start(a->q, tokens * a->Hq), *const k = start(a->k, tokens * a->Hk);
+    const void *const q_up = start(g->dq_out, tokens * a->Hq), *const k_up = start(g->dk_out, tokens * a->Hk);
+    const void *const dq = start(g->dq, tokens * a->Hq), *const dk = start(g->dk, tokens * a->Hk);
+    FALCON_NEED(apart({dq, dk, g->dwq, g->dwk}, {q, k}) && apart({dq}, {k_up}) && apart({dk}, {q_up}));
     FALCON_NEED(ok_array(g->dwq, false) && ok_array(g->dwk, false));
     if (g->dwq || g->dwk) FALCON_TRY(check_workspace(workspace, workspace_bytes, qknorm_bwd_workspace(*a)));
     int sms = 0;

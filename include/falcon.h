@@ -317,7 +317,8 @@ FALCON_API falcon_status_t falcon_decode_step(int rule, int io_dtype, int N, int
  *    an output or gradient must not overlap). Pointers of views need the alignment of their
  *    element only; when pointers and strides are 16-byte multiples, wider accesses are used.
  *  - Outputs and gradients must not overlap inputs or each other, except where an entry point
- *    says so.
+ *    says so. A sequence, state or gradient that starts where another one of the call does is refused
+ *    (INVALID_ARG); other overlaps are not looked for.
  *  - Parameters (weights, biases, A, D, frequencies) and all gradients are fp32, whatever
  *    io_dtype is; gradients are views too where the tensor they belong to is one.
  *  - `lengths`: NULL, or B int32 on the device. Sequence b then has lengths[b] tokens (clamped to

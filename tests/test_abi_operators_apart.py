@@ -1,0 +1,111 @@
+"""Host checks of the operators around the memory: an output that starts where an input or another output does is
+refused (no kernel runs), except where the header allows it."""
+import ctypes
+
+import pytest
+import torch
+
+from test_abi_operators import (CUDA, INVALID, L, OK, conv, conv_grads, qknorm, qknorm_grads, scan, scan_grads,  # noqa: F401
+                                view)
+
+R = ctypes.byref
+HERE = pytest.mark.skipif(torch.cuda.is_available(), reason="a well-formed call would run")
+
+
+def same(a, b, src, dst):
+    """Field dst of b becomes field src of a."""
+    setattr(b, dst, getattr(a, src))
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "delta", "z"])
+def test_scan_output_on_an_input(L, name):
+    a = scan(dk=64)     # rows of one width
+    a.z = view(0x30000, 2, 3, 10, 64)
+    same(a, a, name, "o")
+    assert L.falcon_scan_fwd(R(a), None, 0, None) == INVALID
+    a = scan(dk=64, T=1, S0=0x70000, S_out=0x70000)
+    a.z = view(0x30000, 2, 3, 1, 64)
+    same(a, a, name, "o")
+    assert L.falcon_scan_step(R(a), None) == INVALID
+
+
+def test_scan_states_on_sequences(L):
+    a = scan(io_dtype=0, S0=0x70000, S_out=0x3000)      # v
+    assert L.falcon_scan_fwd(R(a), None, 0, None) == INVALID
+    a = scan(io_dtype=0, S_out=0x6000)                  # o
+    assert L.falcon_scan_fwd(R(a), None, 0, None) == INVALID
+    a = scan(io_dtype=0, S0=0x6000)
+    assert L.falcon_scan_fwd(R(a), None, 0, None) == INVALID
+
+
+@pytest.mark.parametrize("grad", ["dq", "dk", "dv", "ddelta", "dz"])
+@pytest.mark.parametrize("other", ["dO", "q", "k", "v", "delta", "z"])
+def test_scan_gradients_on_inputs(L, grad, other):
+    a, g = scan(dk=64, io_dtype=0), scan_grads(dq=view(0x22000, 2, 3, 10, 64), dk=view(0x23000, 2, 3, 10, 64), dz=view(0x26000, 2, 3, 10, 64))
+    a.z = view(0x30000, 2, 3, 10, 64)
+    same(g if other == "dO" else a, g, other, grad)
+    assert L.falcon_scan_bwd(R(a), R(g), 0x10000, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(dq=view(0x23000, 2, 3, 10, 16)), dict(dv=view(0x25000, 2, 3, 10, 64)), dict(dA=0x24000),
+                                dict(dS0=0x20000), dict(dD=0x20000)])
+def test_scan_gradients_on_each_other(L, kw):
+    assert L.falcon_scan_bwd(R(scan()), R(scan_grads(**kw)), 0x10000, 1 << 40, None) == INVALID
+
+
+def test_scan_gradient_of_the_state_on_the_state(L):
+    assert L.falcon_scan_bwd(R(scan(S0=0x40000)), R(scan_grads(dS0=0x40000)), 0x10000, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(state=0x2000), dict(state_out=0x2000), dict(state_out=0x1000)])
+def test_conv_outputs(L, kw):
+    assert L.falcon_conv_fwd(R(conv(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("a,g", [
+    (dict(), dict(dstate_out=0xa000, dstate=0xa000)),      # a row of dstate is written before dstate_out's is read
+    (dict(state=0xa000), dict(dstate=0xa000)), (dict(), dict(dbias=0x9000)), (dict(), dict(dstate=0x8000)),
+    (dict(io_dtype=0), dict(dx=view(0x1000, 2, 3, 10, 64))), (dict(), dict(dw=0x7000)), (dict(), dict(dstate_out=0x8000))])
+def test_conv_gradients(L, a, g):
+    assert L.falcon_conv_bwd(R(conv(**a)), R(conv_grads(**g)), 0x10000, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(q_out=view(0x2000, 2, 3, 10, 64)), dict(k_out=view(0x1000, 2, 1, 10, 64)),
+                                dict(k_out=view(0x3000, 2, 1, 10, 64))])
+def test_qknorm_outputs(L, kw):
+    assert L.falcon_qknorm_fwd(R(qknorm(**kw)), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [dict(dq=view(0x12000, 2, 3, 10, 64)), dict(dk=view(0x11000, 2, 1, 10, 64)), dict(dk=view(0x13000, 2, 1, 10, 64)),
+                                dict(dq=view(0x1000, 2, 3, 10, 64)), dict(dwq=0x13000)])
+def test_qknorm_gradients(L, kw):
+    assert L.falcon_qknorm_bwd(R(qknorm(io_dtype=0)), R(qknorm_grads(**kw)), 0x10000, 1 << 40, None) == INVALID
+
+
+@HERE
+def test_what_the_header_allows_is_not_refused(L):
+    """In place where an entry point says so, inputs on each other, and equal addresses of what is empty: these calls
+    get as far as looking for a device."""
+    assert L.falcon_conv_fwd(R(conv(state=0x4000, state_out=0x4000)), None) == CUDA
+    assert L.falcon_conv_fwd(R(conv(K=1, state=0x2000, state_out=0x1000)), None) == CUDA
+    assert L.falcon_conv_fwd(R(conv(T=0, state_out=0x1000)), None) == CUDA
+    a = scan(dk=64, S0=0x70000, S_out=0x70000)
+    a.k, a.v, a.delta, a.z = a.q, a.q, a.q, a.q
+    assert L.falcon_scan_fwd(R(a), None, 0, None) == CUDA
+    assert L.falcon_scan_bwd(R(a), R(scan_grads(dS_T=0x40000, dS0=0x40000, dq=view(0x32000, 2, 3, 10, 64), dk=view(0x33000, 2, 3, 10, 64))),
+                             0x10000, 1 << 40, None) == CUDA
+    a = qknorm()
+    a.q_out, a.k_out = a.q, a.k
+    assert L.falcon_qknorm_fwd(R(a), None) == CUDA
+    a.k = a.q
+    a.k_out = view(0x4000, 2, 1, 10, 64)
+    a.q_out = view(0x3000, 2, 3, 10, 64)
+    assert L.falcon_qknorm_fwd(R(a), None) == CUDA
+    g = qknorm_grads()
+    g.dq, g.dk = g.dq_out, g.dk_out
+    assert L.falcon_qknorm_bwd(R(qknorm()), R(g), None, 0, None) == CUDA
+    a = qknorm(Hk=0, k_out=view(0x3000, 2, 0, 10, 64))
+    assert L.falcon_qknorm_fwd(R(a), None) == CUDA
+    none = scan(B=0)
+    none.o = none.q
+    assert L.falcon_scan_fwd(R(none), None, 0, None) == OK
