@@ -487,6 +487,18 @@ def _conv_args(x, w, bias, act, state, lengths, shape, state_shape, y, state_out
         _arr(state, "state", state_shape, io, dev), _arr(state_out, "state_out", state_shape, io, dev))
 
 
+def make_conv_args(x, w, *, bias=None, act="silu", state=None, lengths=None, y=None, state_out=None) -> FalconConvArgs:
+    """The argument struct of falcon_conv_fwd / _bwd for these tensors, for falcon_conv_bwd_workspace_size."""
+    _rank(x, "x", 4)
+    _rank(w, "w", 3)
+    B, H, T, d = shape = tuple(x.shape)
+    return FalconConvArgs.from_buffer_copy(_conv_args(x, w, bias, act, state, lengths, shape, (B, H, max(w.shape[2] - 1, 0), d), y, state_out))
+
+
+def falcon_conv_bwd_workspace_size(args: FalconConvArgs) -> int:
+    return int((_lib or lib()).falcon_conv_bwd_workspace_size(ctypes.byref(args)))
+
+
 def falcon_conv_fwd(x, w, *, bias=None, act="silu", state=None, lengths=None, y=None, state_out=None,
                     want_state=False, stream=None):
     """Causal depthwise convolution over the last K tokens: x (B, H, T, d), w (H, d, K) fp32. Returns
@@ -528,7 +540,8 @@ def falcon_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lengths=None
                     workspace=None, stream=None):
     """Gradients of falcon_conv_fwd for dy (B, H, T, d) fp32 and dstate_out (B, H, K - 1, d) fp32 or None.
     Returns a dict of fp32 tensors dx (token-major rows like a projection's, seen as (B, H, T, d), unless
-    given), dw, dbias (None without bias) and dstate (None without state)."""
+    given), dw, dbias (None without bias) and dstate (None without state). ``workspace``: a CUDA tensor of at least
+    falcon_conv_bwd_workspace_size(make_conv_args(x, w)) bytes, or None to allocate one here for the call."""
     _rank(x, "x", 4)
     _rank(w, "w", 3)
     f32, dev = torch.float32, x.device
@@ -575,15 +588,28 @@ def _scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, len
         _arr(S0, "S0", state, f32, dev), _arr(S_out, "S_out", state, f32, dev))
 
 
+def make_scan_args(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softplus=True, S0=None, lengths=None, o=None,
+                   S_out=None) -> FalconScanArgs:
+    """The argument struct of falcon_scan_fwd / _bwd for these tensors, for falcon_scan_workspace_size and
+    falcon_scan_bwd_workspace_size."""
+    sizes, vs, ks = _scan_shapes(k, v, 4)
+    return FalconScanArgs.from_buffer_copy(_scan_args(sizes, vs, ks, q, k, v, delta, A, D, z, delta_bias, softplus, lengths, S0, o, S_out))
+
+
 def falcon_scan_workspace_size(args: FalconScanArgs) -> int:
     return int((_lib or lib()).falcon_scan_workspace_size(ctypes.byref(args)))
+
+
+def falcon_scan_bwd_workspace_size(args: FalconScanArgs) -> int:
+    return int((_lib or lib()).falcon_scan_bwd_workspace_size(ctypes.byref(args)))
 
 
 def falcon_scan_fwd(q, k, v, delta, A, *, D=None, z=None, delta_bias=None, softplus=True, S0=None, lengths=None,
                     o=None, S_out=None, want_state=True, workspace=None, stream=None):
     """Selective scan: q, k (B, H, T, dk), v, delta and z (B, H, T, dv), A (H, dv, dk), D and delta_bias
     (H, dv), S0 (B, H, dv, dk); parameters and states fp32. Returns (o, S_out). With few channels the
-    sequence is split, for which a workspace is made here unless one is given (a smaller one runs it whole)."""
+    sequence is split, for which a workspace of falcon_scan_workspace_size(make_scan_args(q, k, v, delta, A)) bytes is
+    made here unless one is given (a smaller one runs it whole)."""
     sizes, vs, ks = _scan_shapes(k, v, 4)
     B, H, T, dk, dv = sizes
     dev = v.device
@@ -618,7 +644,8 @@ def falcon_scan_bwd(q, k, v, delta, A, dO, *, D=None, z=None, delta_bias=None, s
                     dS_T=None, workspace=None, stream=None):
     """Gradients of falcon_scan_fwd for dO (B, H, T, dv) fp32 and dS_T (B, H, dv, dk) fp32 or None. Returns a
     dict of fp32 tensors dq, dk, dv, ddelta, dA and, for the inputs that were given, dD, ddelta_bias, dz, dS0
-    (None otherwise). Sequence gradients are token-major rows seen as (B, H, T, d)."""
+    (None otherwise). Sequence gradients are token-major rows seen as (B, H, T, d). ``workspace``: a CUDA tensor of at
+    least falcon_scan_bwd_workspace_size(make_scan_args(q, k, v, delta, A)) bytes, or None to allocate one here."""
     sizes, vs, ks = _scan_shapes(k, v, 4)
     B, H, T, dk, dv = sizes
     dev, f32 = v.device, torch.float32
@@ -665,6 +692,18 @@ def _qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, 
         _arr(positions, "positions", (B, T), torch.int32, dev), _arr(lengths, "lengths", (B,), torch.int32, dev))
 
 
+def make_qknorm_args(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, layout="half", freq=None, positions=None,
+                     lengths=None, q_out=None, k_out=None) -> FalconQknormArgs:
+    """The argument struct of falcon_qknorm_fwd / _bwd for these tensors, for falcon_qknorm_bwd_workspace_size (which
+    needs freq where rot > 0)."""
+    x, qs, ks = _qknorm_shapes(q, k)
+    return FalconQknormArgs.from_buffer_copy(_qknorm_args(x, qs, ks, q, k, q_out, k_out, wq, wk, norm, eps, rot, layout, freq, positions, lengths))
+
+
+def falcon_qknorm_bwd_workspace_size(args: FalconQknormArgs) -> int:
+    return int((_lib or lib()).falcon_qknorm_bwd_workspace_size(ctypes.byref(args)))
+
+
 def falcon_qknorm_fwd(q, k, *, wq=None, wk=None, norm="rms", eps=1e-6, rot=0, layout="half", freq=None, positions=None,
                       lengths=None, q_out=None, k_out=None, stream=None):
     """Norm of each head's rows of q (B, Hq, T, d) and k (B, Hk, T, d) with the rotation of their first ``rot``
@@ -686,7 +725,8 @@ def falcon_qknorm_bwd(q, k, dq_out, dk_out, *, wq=None, wk=None, norm="rms", eps
                       positions=None, lengths=None, workspace=None, stream=None):
     """Gradients of falcon_qknorm_fwd for dq_out, dk_out (fp32, the shapes of q and k). Returns a dict of fp32
     tensors dq, dk (token-major rows seen as (B, H, T, d); None where q or k is), dwq and dwk (None without
-    the weight)."""
+    the weight). ``workspace`` (used where a weight is given): a CUDA tensor of at least
+    falcon_qknorm_bwd_workspace_size(make_qknorm_args(q, k)) bytes, or None to allocate one here for the call."""
     x, qs, ks = _qknorm_shapes(q, k)
     dev, f32 = x.device, torch.float32
     ctx, raw = _on(dev, stream)
