@@ -315,6 +315,7 @@ falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *a, const falcon_scan_g
                       {start(g->dO, rows), start(a->q, rows), start(a->k, rows), start(a->v, rows), start(a->delta, rows),
                        start(a->z, rows), a->S0}));
     if (a->H == 0) return FALCON_OK;
+    if (!scan_bwd_fits(*a)) return FALCON_ERR_UNSUPPORTED;
     FALCON_TRY(check_workspace(workspace, workspace_bytes, scan_bwd_workspace(*a)));
     int sms = 0;
     FALCON_TRY(device(&sms));

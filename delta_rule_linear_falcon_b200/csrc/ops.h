@@ -36,6 +36,7 @@ ScanPlan scan_plan(const falcon_scan_args_t &a, int num_sms);
 cudaError_t launch_scan_fwd(const falcon_scan_args_t &a, const ScanPlan &plan, float *ws, cudaStream_t s);
 cudaError_t launch_scan_step(const falcon_scan_args_t &a, int num_sms, cudaStream_t s);
 size_t scan_bwd_workspace(const falcon_scan_args_t &a);
+bool scan_bwd_fits(const falcon_scan_args_t &a);   // its grids
 cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads_t &g, float *ws, cudaStream_t s);
 
 // norm of queries and keys (qknorm.cu)

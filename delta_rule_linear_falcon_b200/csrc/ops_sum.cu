@@ -18,7 +18,12 @@ struct SumJobs {
 // 10240 of 108 rows 4.7 us, 256 of 296 rows 5.7 us (one chain and 128 columns a block: 5.1, 9.1 and 18 us; 32 chains:
 // slower by a tenth to threefold). Blocks are numbered through the jobs: a grid of the widest job for each of them
 // took 16 us for the first of these.
-__global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs jobs, int nparts) {
+// LONG: more rows than kLong (one for each of very many short sequences). A chain then hands its sum over after each kRun
+// batches, so that it loses no more than a short one. On its own, since that costs the short sums up to a microsecond.
+constexpr int kBatch = 8, kRun = 1024, kLong = kRun * kBatch * kChains;
+
+template <bool LONG>
+__global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs jobs, int nparts, long long runs) {
     __shared__ float acc[kChains][kSumCols + 1];
     int which = 0;
 #pragma unroll
@@ -28,9 +33,25 @@ __global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs 
     const long long e = (long long)(blockIdx.x - jobs.first[which]) * kSumCols + threadIdx.x;
     float s = 0.f;
     if (e < j.n) {
-        constexpr int U = 8;
+        constexpr int U = kBatch;
         const float *p = j.part + threadIdx.y * j.stride + e;
         const long long step = kChains * j.stride;
+        float done = 0.f;
+        if (LONG) {
+            for (long long r = 0; r < runs; ++r) {
+#pragma unroll 4
+                for (int k = 0; k < kRun; ++k) {
+                    float x[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) x[u] = p[u * step];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) s += x[u];
+                    p += U * step;
+                }
+                done += s;
+                s = 0.f;
+            }
+        }
         int i = threadIdx.y;
         for (; i + (U - 1) * kChains < nparts; i += U * kChains) {
             float x[U];
@@ -45,6 +66,7 @@ __global__ void __launch_bounds__(kSumCols * kChains) column_sum_kernel(SumJobs 
         for (int u = 0; u < U; ++u) x[u] = i + u * kChains < nparts ? p[u * step] : 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u) s += x[u];
+        if (LONG) s += done;
     }
     acc[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
@@ -68,8 +90,10 @@ cudaError_t launch_column_sums(const SumJob *jobs, int njobs, long long nparts, 
         blocks += (jobs[i].n + kSumCols - 1) / kSumCols;
     }
     if (js.count == 0) return cudaSuccess;
-    if (blocks > kMaxGrid || nparts > 0x7fffffff / 16) return cudaErrorInvalidConfiguration;
-    column_sum_kernel<<<(unsigned)blocks, dim3(kSumCols, kChains), 0, s>>>(js, (int)nparts);
+    if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
+    const dim3 block(kSumCols, kChains);
+    if (nparts > kLong) column_sum_kernel<true><<<(unsigned)blocks, block, 0, s>>>(js, (int)(nparts % kLong), nparts / kLong);
+    else column_sum_kernel<false><<<(unsigned)blocks, block, 0, s>>>(js, (int)nparts, 0);
     return cudaGetLastError();
 }
 

@@ -569,6 +569,7 @@ int bwd_channels(int sl) {
 struct BwdSizes {
     int nseg, walk, nwalk, ngrp, cols;
     int block;          // walks of a block of step 1
+    long long groups1;  // blocks of step 1 for each of its stretches of walks
     long long rows;     // channels of all sequences
     long long qk;       // floats of all parts of dq and dk
     long long floats;   // the workspace
@@ -601,10 +602,10 @@ BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
     z.nwalk = (z.nseg + z.walk - 1) / z.walk;
     // step 1: blocks of as many walks as fill the SMs best, with a prologue of about 24 tokens' time
     const int cpb = kScanThreads / (a.dk <= 16 ? 1 : a.dk <= 32 ? 2 : a.dk <= 64 ? 4 : 8);
-    const long long groups1 = (long long)a.B * a.H * ((a.dv + cpb - 1) / cpb);
+    z.groups1 = (long long)a.B * a.H * ((a.dv + cpb - 1) / cpb);
     z.block = 1;
     for (int n = 1; n <= 16; ++n) {
-        const double cost = (double)turns(groups1 * ((z.nwalk + n - 1) / n)) * (n * z.walk * kSeg + 24);
+        const double cost = (double)turns(z.groups1 * ((z.nwalk + n - 1) / n)) * (n * z.walk * kSeg + 24);
         if (n == 1 || cost < best) {
             best = cost;
             z.block = n;
@@ -618,7 +619,6 @@ BwdSizes bwd_sizes(const falcon_scan_args_t &a) {
 template <typename IO, int SL>
 cudaError_t scan_bwd_t(const falcon_scan_args_t &a, const falcon_scan_grads_t &g, const ScanBwdWork &w, int ngrp, cudaStream_t s) {
     const long long blocks = (long long)ngrp * a.B * a.H * w.s.nwalk;
-    if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
     const size_t smem = BwdShape<SL>::kBytes;
     const auto kern = w.s.nwalk == 1 ? scan_bwd_kernel<IO, SL, true> : scan_bwd_kernel<IO, SL, false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -640,6 +640,15 @@ cudaError_t scan_bwd_io(const falcon_scan_args_t &a, const falcon_scan_grads_t &
 }
 
 }  // namespace
+
+// Every launch's grid, so that a call that one of them would refuse writes nothing.
+bool scan_bwd_fits(const falcon_scan_args_t &a) {
+    const BwdSizes z = bwd_sizes(a);
+    const long long bh = (long long)a.B * a.H, walks = (z.nwalk + z.block - 1) / z.block;
+    const auto fits = [](long long n, long long times) { return times == 0 || n <= kMaxGrid / times; };
+    return fits(z.groups1, walks) && fits(z.ngrp * bh, z.nwalk) && (z.rows * z.cols + 255) / 256 <= kMaxGrid &&
+           (z.ngrp <= 1 || (bh * a.T * a.dk + 255) / 256 <= kMaxGrid) && ((long long)a.H * a.dv * (a.dk + 2LL)) / 32 + 3 <= kMaxGrid;
+}
 
 size_t scan_bwd_workspace(const falcon_scan_args_t &a) { return sizeof(float) * (size_t)bwd_sizes(a).floats; }
 
@@ -676,7 +685,6 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
         }
         if (z.nwalk != 1) {
             const long long jb = (z.rows * z.cols + 255) / 256;
-            if (jb > kMaxGrid) return cudaErrorInvalidConfiguration;
             scan_join_kernel<<<dim3((unsigned)jb, 2), 256, 0, s>>>(a, w.s, z.cols, g.dS_T, g.dS0);
             e = cudaGetLastError();
             if (e != cudaSuccess) return e;
@@ -686,7 +694,6 @@ cudaError_t launch_scan_bwd(const falcon_scan_args_t &a, const falcon_scan_grads
             if (e != cudaSuccess) return e;
             if (z.ngrp > 1) {
                 const long long blocks = ((long long)a.B * a.H * a.T * a.dk + 255) / 256;
-                if (blocks > kMaxGrid) return cudaErrorInvalidConfiguration;
                 scan_qk_sum_kernel<<<dim3((unsigned)blocks, 2), 256, 0, s>>>(a, g, w.qk, z.ngrp);
                 e = cudaGetLastError();
                 if (e != cudaSuccess) return e;

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from test_abi_operators import (CUDA, INVALID, L, OK, conv, conv_grads, qknorm, qknorm_grads, scan, scan_grads,  # noqa: F401
+from test_abi_operators import (CUDA, INVALID, L, OK, UNSUPPORTED, conv, conv_grads, qknorm, qknorm_grads, scan, scan_grads,  # noqa: F401
                                 view)
 
 R = ctypes.byref
@@ -109,3 +109,17 @@ def test_what_the_header_allows_is_not_refused(L):
     none = scan(B=0)
     none.o = none.q
     assert L.falcon_scan_fwd(R(none), None, 0, None) == OK
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=8, H=8, T=1000, dk=128, dv=1 << 27),          # the joins' grid: states of 2^33 channels
+    dict(B=1 << 20, H=1, T=1 << 15, dk=128, dv=17),      # the sums of dq and dk over a head's two blocks
+    dict(B=1 << 24, H=1, T=1 << 16, dk=1, dv=1)])        # the main grid: 2^24 sequences of 128 walks
+def test_scan_backward_refuses_before_its_first_launch(L, kw):
+    a, g = scan(**kw), scan_grads()
+    for s, names in ((a, ("q", "k", "v", "delta")), (g, ("dO", "dq", "dk", "dv", "ddelta"))):
+        for i, n in enumerate(names):
+            d = kw["dk"] if n in ("q", "k", "dq", "dk") else kw["dv"]
+            setattr(s, n, view((0x100000 if s is g else 0x200000) + 0x1000 * i, kw["B"], kw["H"], kw["T"], d))
+    assert L.falcon_scan_bwd_workspace_size(R(a)) > 1 << 40
+    assert L.falcon_scan_bwd(R(a), R(g), 0x10000, (1 << 64) - 16, None) == UNSUPPORTED

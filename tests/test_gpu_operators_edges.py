@@ -67,3 +67,27 @@ def test_scan_nan_in_A_is_seen(F):
     g["A"][0, 3, 5] = float("nan")
     _, S = F.falcon_scan_fwd(**g)
     assert S[0, 0, 3, 5].isnan() and int(S.isnan().sum()) == 1
+
+
+# ------------------------------------------------------------------ gradients of very many sequences
+
+def test_conv_backward_of_2_27_sequences(F):
+    """A partial row for each sequence. Whole numbers that fp32 sums hold exactly."""
+    N = 2 ** 27 + 3
+    at = torch.arange(N, dtype=torch.int32, device="cuda")
+    x = ((at % 7 == 0).to(torch.bfloat16) - (at % 11 == 0).to(torch.bfloat16)).view(N, 1, 1, 1)
+    dy = (at % 13 - 6).float().view(N, 1, 1, 1)
+    one = torch.ones(1, 1, 1, device="cuda")
+    g = F.falcon_conv_bwd(x, one, dy, bias=torch.zeros(1, 1, device="cuda"), act="none", dx=torch.empty(N, 1, 1, 1, device="cuda"))
+    assert torch.equal(g["dx"], dy)
+    assert int(g["dbias"]) == int(dy.sum(dtype=torch.float64)) and int(g["dw"]) == int((dy * x.float()).sum(dtype=torch.float64))
+
+
+def test_long_column_sums(F):
+    """dbias over 2^21 sequences of one token, all terms near 1: a chain of 2^18 fp32 additions in sequence would be off by
+    up to 2^18 half steps of 2^-24, 1.6e-2. Handed over after each 2^13, it is 2^13 + 2^5 + a block's few: 5e-4 at worst."""
+    N = 2 ** 21
+    dy = 1 + torch.rand(N, 1, 1, 1, generator=torch.Generator().manual_seed(5)).cuda() * 2 ** -3
+    g = F.falcon_conv_bwd(torch.ones_like(dy), torch.ones(1, 1, 1, device="cuda"), dy, bias=torch.zeros(1, 1, device="cuda"), act="none")
+    want = float(dy.sum(dtype=torch.float64))
+    assert abs(float(g["dbias"]) - want) <= (2 ** 13 + 2 ** 5 + 16) * 2.0 ** -24 * want
