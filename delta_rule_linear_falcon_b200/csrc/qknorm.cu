@@ -563,6 +563,7 @@ constexpr int kBwdBlocks = 148 * 2;
 // the GPU holds).
 NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
     constexpr long long kWanted = 148LL * 1536;
+    constexpr int kMaxParts = 65535;   // of a grid's second axis
     NormShape s;
     const int heads = a.Hq + a.Hk, per = kNormThreads / lanes;
     const long long all = (long long)a.B * a.T;
@@ -570,8 +571,10 @@ NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
     s.heads = heads;
     s.parts = 1;
     while (s.heads > 1 && all * lanes * s.parts < kWanted) {
-        s.heads = (s.heads + 1) / 2;
-        s.parts = (heads + s.heads - 1) / s.heads;
+        const int fewer = (s.heads + 1) / 2, parts = (heads + fewer - 1) / fewer;
+        if (parts > kMaxParts) break;
+        s.heads = fewer;
+        s.parts = parts;
     }
     s.units = s.groups * heads;
     s.blocks = (int)(s.units < kBwdBlocks ? s.units : kBwdBlocks);
@@ -585,7 +588,7 @@ cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t 
     if (g) {
         qknorm_bwd_kernel<IO, V, LANES, NV, HALF><<<s.blocks, kNormThreads, smem, st>>>(a, *g, s, part);
     } else {
-        if (s.groups > kMaxGrid || s.parts > 65535) return cudaErrorInvalidConfiguration;
+        if (s.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
         qknorm_fwd_kernel<IO, V, LANES, NV, HALF><<<dim3((unsigned)s.groups, (unsigned)s.parts), kNormThreads, smem, st>>>(a, s);
     }
     return cudaGetLastError();

@@ -325,6 +325,8 @@ FALCON_API falcon_status_t falcon_decode_step(int rule, int io_dtype, int N, int
  *    [0, T]); what lies at t >= lengths[b] is not read, rows of forward outputs there are left as
  *    they were, rows of gradients there are written 0, and final states are those after the last
  *    token of the sequence.
+ *  - Sizes: T <= 2^30; B H and H d below 2^31 (also H dk and H dv); B H T d <= 2^50. Calls that would take more than
+ *    2^31 - 1 blocks are UNSUPPORTED, and write nothing.
  *  - Sums over tokens are taken in a fixed order: repeated calls give the same bits.
  *  - A workspace is used only while the call's kernels run on `stream`; calls that can overlap on the GPU (other
  *    streams, graphs replayed side by side) need workspaces of their own. The first call of the library on a device
@@ -480,7 +482,7 @@ FALCON_API falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *args, const
  * Angles are reduced in fp64, so far positions keep their accuracy; everything else is fp32.
  * positions NULL: t. rot = 0: no rotation. Hk (or Hq) = 0 leaves out that tensor. q_out may be the
  * same memory as q with the same strides (likewise k). One token per sequence is T = 1.
- * Supported: 1 <= d <= 256; rot even, 0 <= rot <= d; fp32 or bf16.
+ * Supported: 1 <= d <= 256; Hq, Hk <= 65536; rot even, 0 <= rot <= d; fp32 or bf16.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 typedef enum { FALCON_NORM_NONE = 0, FALCON_NORM_RMS = 1, FALCON_NORM_L2 = 2 } falcon_norm_t;

@@ -91,3 +91,24 @@ def test_long_column_sums(F):
     g = F.falcon_conv_bwd(torch.ones_like(dy), torch.ones(1, 1, 1, device="cuda"), dy, bias=torch.zeros(1, 1, device="cuda"), act="none")
     want = float(dy.sum(dtype=torch.float64))
     assert abs(float(g["dbias"]) - want) <= (2 ** 13 + 2 ** 5 + 16) * 2.0 ** -24 * want
+
+
+# ------------------------------------------------------------------ norm of very many heads
+
+@pytest.mark.parametrize("io,Hq,Hk,d,T", [("f32", 65000, 5000, 16, 1), ("bf16", 65536, 65536, 4, 1), ("bf16", 65536, 1, 3, 2)])
+def test_qknorm_of_many_heads(F, io, Hq, Hk, d, T):
+    """A token's heads in as many blocks as a grid takes: the same bits as calls on a thousand heads each."""
+    r = torch.Generator(device="cuda").manual_seed(54)
+    rand = lambda *s: torch.randn(*s, generator=r, device="cuda")
+    q, k, wq, wk = rand(1, Hq, T, d).to(IO[io]), rand(1, Hk, T, d).to(IO[io]), rand(d), rand(d)
+    rot = d // 2 * 2
+    kw = dict(wq=wq, wk=wk, rot=rot, freq=torch.rand(rot // 2, generator=r, device="cuda"))
+    qo, ko = F.falcon_qknorm_fwd(q, k, **kw)
+    for x, o in ((q, qo), (k, ko)):
+        name = "wq" if x is q else "wk"
+        for at in range(0, x.shape[1], 1000):
+            few = x[:, at:at + 1000].contiguous()
+            assert torch.equal(F.falcon_qknorm_fwd(few, None, **{**kw, "wq": kw[name]})[0], o[:, at:at + 1000])
+    want = O.qknorm(q[:, -50:].double().cpu(), w=wq.double().cpu(), rot=rot, freq=kw["freq"].cpu())
+    close(qo[:, -50:], want, 2.0 ** -18 * O.qknorm(q[:, -50:].double().cpu(), w=wq.double().cpu()).abs().amax(-1, keepdim=True)
+          + half_step(io, want))
