@@ -155,8 +155,18 @@ template <typename E, bool HALF> struct Row<E, 1, HALF> {
     static __device__ __forceinline__ void st(E *row, Place at, const float (&x)[1]) { P::st(row + at.a, x); }
 };
 
+// Pairs 2 i and 2 i + 1 of pack p where they turn, 0 where they do not: there a sine of 0 times a partner that is not
+// finite would be NaN. (FALCON_ROT_HALF: all of a pack's pairs turn, or none.)
+template <int V>
+__device__ __forceinline__ f32x2 turning(f32x2 x, int p, int i, int rot) {
+    float lo, hi;
+    unpack2(x, lo, hi);
+    const int first = p * V + 4 * i;   // as channels of FALCON_ROT_PAIRS
+    return pack2(first < rot ? lo : 0.f, first + 2 < rot ? hi : 0.f);
+}
+
 // A lane's part of a token's rotation: the factors of its pairs.
-template <int V, int LANES, int NV, bool HALF> struct Turn {
+template <int V, int LANES, int NV, bool HALF, bool SOME> struct Turn {
     static constexpr int H = V / 2;
     float c[NV][H], s[NV][H];
     __device__ __forceinline__ void load(const falcon_qknorm_args_t &a, int lane, const float2 *cs, float sign) {
@@ -186,8 +196,9 @@ template <int V, int LANES, int NV, bool HALF> struct Turn {
             }
     }
 };
-// One channel a pack: the factor of the channel itself, its partner, and the partner's factor with its sign.
-template <int LANES, int NV, bool HALF> struct Turn<1, LANES, NV, HALF> {
+// One channel a pack: the factor of the channel itself, its partner, and the partner's factor with its sign. SOME:
+// channels that do not turn have the 0 behind the row for a partner.
+template <int LANES, int NV, bool HALF, bool SOME> struct Turn<1, LANES, NV, HALF, SOME> {
     float c[NV], s[NV];
     int from[NV];
     __device__ __forceinline__ void load(const falcon_qknorm_args_t &a, int lane, const float2 *cs, float sign) {
@@ -197,7 +208,7 @@ template <int LANES, int NV, bool HALF> struct Turn<1, LANES, NV, HALF> {
             const int p = lane + m * LANES;
             c[m] = 1.f;
             s[m] = 0.f;
-            from[m] = p;
+            from[m] = SOME ? kMaxWidth : p;
             if (p < a.rot) {
                 const bool hi = HALF ? p >= half : (p & 1) != 0;
                 from[m] = HALF ? (hi ? p - half : p + half) : p ^ 1;
@@ -217,17 +228,31 @@ template <int LANES, int NV, bool HALF> struct Turn<1, LANES, NV, HALF> {
     }
 };
 
-template <typename IO, int V, int LANES, int NV, bool HALF>
-__global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_args_t a, NormShape s) {
+// Which channels turn: none, each one, or some. A pair that does not turn must not see its partner (a sine of 0 times
+// infinity is NaN), and choosing costs registers, so the first two are compiled on their own.
+enum TurnKind : int { kTurnNone, kTurnAll, kTurnSome };
+
+// Blocks an SM that the last kind is held to (0: as it comes), measured on bf16 B8 H16+16 T4096 d128 with 64 channels
+// turned, in pairs: four 95 us, as it comes (three) 103; with d 64 and 6 turned, packs of four: six 51, as it comes 58. In
+// halves, where a pack turns or does not: as it comes 94, four 102. One channel a pack, d 199 fp32: four 93, as it comes 101.
+constexpr int fwd_blocks(int es, int V, int NV, bool half, int turn) {
+    if (turn != kTurnSome) return 0;
+    if (V == 1) return NV == 8 ? 4 : 0;
+    return half || NV > 1 ? 0 : V == 8 ? 4 : es == 2 ? 6 : 5;
+}
+
+template <typename IO, int V, int LANES, int NV, bool HALF, int TURN>
+__global__ void __launch_bounds__(kNormThreads, fwd_blocks(sizeof(IO), V, NV, HALF, TURN)) qknorm_fwd_kernel(falcon_qknorm_args_t a, NormShape s) {
     typedef Row<IO, V, HALF> R;
     constexpr int G = kNormThreads / LANES;       // groups of lanes, tokens of a block
     constexpr int kRows = NV >= 4 ? 1 : 4 / NV;   // rows in flight
     extern __shared__ __align__(16) float2 cs[];
-    __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
+    __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth + (TURN == kTurnSome) : 1];
     float *stage = stage_all[V == 1 ? threadIdx.x >> 5 : 0];
+    if (V == 1 && TURN == kTurnSome && threadIdx.x % 32 == 0) stage[kMaxWidth] = 0.f;   // read behind a row's barriers
     const long long tok0 = (long long)blockIdx.x * G;
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
-    Turn<V, LANES, NV, HALF> turn;
+    Turn<V, LANES, NV, HALF, TURN == kTurnSome> turn;
     if (a.rot > 0) {
         angles<V>(a, tok0, G, cs);
         __syncthreads();
@@ -307,8 +332,23 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_
                     for (int m = 0; m < NV; ++m)
 #pragma unroll
                         for (int i = 0; i < Q; ++i) {
-                            const f32x2 y1 = mul2(ri2, fma2(x1[m][i], c1[m][i], mul2(x2[m][i], s2[m][i])));
-                            const f32x2 y2 = mul2(ri2, fma2(x2[m][i], c2[m][i], mul2(x1[m][i], s1[m][i])));
+                            f32x2 y1, y2;
+                            if (TURN == kTurnNone) {
+                                y1 = mul2(ri2, mul2(x1[m][i], c1[m][i]));
+                                y2 = mul2(ri2, mul2(x2[m][i], c2[m][i]));
+                            } else {
+                                f32x2 z1 = 0ull, z2 = 0ull;
+                                if (TURN == kTurnAll || (lane + m * LANES) * V < a.rot) {
+                                    z1 = mul2(x2[m][i], s2[m][i]);
+                                    z2 = mul2(x1[m][i], s1[m][i]);
+                                    if (TURN == kTurnSome && !HALF) {   // the last pack's pairs may turn in part
+                                        z1 = turning<V>(z1, lane + m * LANES, i, a.rot);
+                                        z2 = turning<V>(z2, lane + m * LANES, i, a.rot);
+                                    }
+                                }
+                                y1 = mul2(ri2, fma2(x1[m][i], c1[m][i], z1));
+                                y2 = mul2(ri2, fma2(x2[m][i], c2[m][i], z2));
+                            }
                             unpack2(y1, x[m][2 * i], x[m][2 * i + 1]);
                             unpack2(y2, x[m][H + 2 * i], x[m][H + 2 * i + 1]);
                         }
@@ -332,7 +372,7 @@ __global__ void __launch_bounds__(kNormThreads) qknorm_fwd_kernel(falcon_qknorm_
     }
 }
 
-template <typename IO, int V, int LANES, int NV, bool HALF>
+template <typename IO, int V, int LANES, int NV, bool HALF, int TURN>
 __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kernel(falcon_qknorm_args_t a, falcon_qknorm_grads_t g, NormShape s,
                                                                   float *part) {
     typedef Row<IO, V, HALF> R;
@@ -340,11 +380,13 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
     constexpr int G = kNormThreads / LANES;
     constexpr int kRows = NV > 1 ? 1 : 2;   // rows worked on together, as many more on their way
     extern __shared__ __align__(16) float2 cs[];
-    __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth : 1];
+    __shared__ float stage_all[V == 1 ? kNormWarps : 1][V == 1 ? kMaxWidth + (TURN == kTurnSome) : 1];
     __shared__ float sw[2][kMaxWidth];
     float *stage = stage_all[V == 1 ? threadIdx.x >> 5 : 0];
+    if (V == 1 && TURN == kTurnSome && threadIdx.x % 32 == 0) stage[kMaxWidth] = 0.f;   // read behind a row's barriers
     const int lane = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     const int heads = a.Hq + a.Hk;
+    const bool plain = TURN != kTurnAll && a.norm == FALCON_NORM_NONE;   // dx is u then, whatever x is
     const float scale = a.norm == FALCON_NORM_RMS ? 1.f / (float)a.d : 1.f;
     constexpr int NP = V > 1 ? V / 2 : 1;
     f32x2 dw2[2][NV][NP];   // V > 1: the first channels of the pairs, then the second
@@ -366,7 +408,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
         const int b = there ? (int)(tok / a.T) : 0, t = there ? (int)(tok - (long long)b * a.T) : 0;
         const bool live = there && t < seq_length(a.lengths, b, a.T);
 
-        Turn<V, LANES, NV, HALF> turn;
+        Turn<V, LANES, NV, HALF, TURN == kTurnSome> turn;
         if (a.rot > 0) {
             __syncthreads();
             angles<V>(a, tok0, G, cs);
@@ -450,13 +492,17 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
                             for (int i = 0; i < Q; ++i) {
                                 u1[m][i] = pack2(u[m][2 * i], u[m][2 * i + 1]);
                                 u2[m][i] = pack2(u[m][H + 2 * i], u[m][H + 2 * i + 1]);
-                                if (a.rot > 0) {
+                                if (TURN == kTurnAll || (TURN == kTurnSome && (lane + m * LANES) * V < a.rot)) {
                                     const f32x2 c = pack2(turn.c[m][2 * i], turn.c[m][2 * i + 1]);
                                     const f32x2 sn = pack2(turn.s[m][2 * i], turn.s[m][2 * i + 1]);
                                     const f32x2 ns = pack2(-turn.s[m][2 * i], -turn.s[m][2 * i + 1]);
-                                    const f32x2 y = fma2(u1[m][i], c, mul2(u2[m][i], ns));
-                                    u2[m][i] = fma2(u2[m][i], c, mul2(u1[m][i], sn));
-                                    u1[m][i] = y;
+                                    f32x2 z1 = mul2(u2[m][i], ns), z2 = mul2(u1[m][i], sn);
+                                    if (TURN == kTurnSome && !HALF) {   // the last pack's pairs may turn in part
+                                        z1 = turning<V>(z1, lane + m * LANES, i, a.rot);
+                                        z2 = turning<V>(z2, lane + m * LANES, i, a.rot);
+                                    }
+                                    u1[m][i] = fma2(u1[m][i], c, z1);
+                                    u2[m][i] = fma2(u2[m][i], c, z2);
                                 }
                                 x1[m][i] = mul2(x1[m][i], ri2);
                                 x2[m][i] = mul2(x2[m][i], ri2);
@@ -475,8 +521,9 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
                         for (int m = 0; m < NV; ++m)
 #pragma unroll
                             for (int i = 0; i < Q; ++i) {
-                                unpack2(mul2(ri2, fma2(x1[m][i], dot2, u1[m][i])), u[m][2 * i], u[m][2 * i + 1]);
-                                unpack2(mul2(ri2, fma2(x2[m][i], dot2, u2[m][i])), u[m][H + 2 * i], u[m][H + 2 * i + 1]);
+                                const f32x2 xa = plain ? 0ull : x1[m][i], xb = plain ? 0ull : x2[m][i];
+                                unpack2(mul2(ri2, fma2(xa, dot2, u1[m][i])), u[m][2 * i], u[m][2 * i + 1]);
+                                unpack2(mul2(ri2, fma2(xb, dot2, u2[m][i])), u[m][H + 2 * i], u[m][H + 2 * i + 1]);
                             }
                     } else {
                         float ss = 0.f, dot = 0.f;
@@ -493,7 +540,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
                         }
                         dot = a.norm == FALCON_NORM_NONE ? 0.f : -lanes_total<LANES>(dot) * scale;
 #pragma unroll
-                        for (int m = 0; m < NV; ++m) u[m][0] = ri * fmaf(x[m][0], dot, u[m][0]);
+                        for (int m = 0; m < NV; ++m) u[m][0] = ri * fmaf(plain ? 0.f : x[m][0], dot, u[m][0]);
                     }
                     if (there && h + r < last) {
 #pragma unroll
@@ -581,17 +628,27 @@ NormShape norm_shape(const falcon_qknorm_args_t &a, int lanes) {
     return s;
 }
 
-template <typename IO, int V, int LANES, int NV, bool HALF>
-cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
+template <typename IO, int V, int LANES, int NV, bool HALF, int TURN>
+cudaError_t norm_launch(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
     const NormShape s = norm_shape(a, LANES);
     const size_t smem = (size_t)(kNormThreads / LANES) * turn_slots(a, V) * sizeof(float2);
     if (g) {
-        qknorm_bwd_kernel<IO, V, LANES, NV, HALF><<<s.blocks, kNormThreads, smem, st>>>(a, *g, s, part);
+        qknorm_bwd_kernel<IO, V, LANES, NV, HALF, TURN><<<s.blocks, kNormThreads, smem, st>>>(a, *g, s, part);
     } else {
         if (s.groups > kMaxGrid) return cudaErrorInvalidConfiguration;
-        qknorm_fwd_kernel<IO, V, LANES, NV, HALF><<<dim3((unsigned)s.groups, (unsigned)s.parts), kNormThreads, smem, st>>>(a, s);
+        qknorm_fwd_kernel<IO, V, LANES, NV, HALF, TURN><<<dim3((unsigned)s.groups, (unsigned)s.parts), kNormThreads, smem, st>>>(a, s);
     }
     return cudaGetLastError();
+}
+
+template <typename IO, int V, int LANES, int NV, bool HALF>
+cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
+    if (a.rot == 0) {   // halves then, see norm_any
+        if constexpr (HALF) return norm_launch<IO, V, LANES, NV, HALF, kTurnNone>(a, g, part, st);
+    } else if (a.rot == a.d && !(g && a.norm == FALCON_NORM_NONE)) {   // (without a norm the gradient has to choose as well)
+        return norm_launch<IO, V, LANES, NV, HALF, kTurnAll>(a, g, part, st);
+    }
+    return norm_launch<IO, V, LANES, NV, HALF, kTurnSome>(a, g, part, st);
 }
 
 template <typename IO, int V, bool HALF>
@@ -621,7 +678,7 @@ cudaError_t norm_io(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *
 }
 
 cudaError_t norm_any(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t *g, float *part, cudaStream_t st) {
-    const bool half = a.rot_layout == FALCON_ROT_HALF;
+    const bool half = a.rot_layout == FALCON_ROT_HALF || a.rot == 0;   // the layouts differ where something turns
     if (a.io_dtype == FALCON_BF16) return half ? norm_io<__nv_bfloat16, 8, true>(a, g, part, st) : norm_io<__nv_bfloat16, 8, false>(a, g, part, st);
     return half ? norm_io<float, 4, true>(a, g, part, st) : norm_io<float, 4, false>(a, g, part, st);
 }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import operators as O
-from test_gpu_operators import F, IO, close, gradients_close, half_step, scan_bound, scan_inputs  # noqa: F401
+from test_gpu_operators import Draw, F, IO, close, gradients_close, half_step, scan_bound, scan_inputs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,61 @@ def test_qknorm_of_many_heads(F, io, Hq, Hk, d, T):
     want = O.qknorm(q[:, -50:].double().cpu(), w=wq.double().cpu(), rot=rot, freq=kw["freq"].cpu())
     close(qo[:, -50:], want, 2.0 ** -18 * O.qknorm(q[:, -50:].double().cpu(), w=wq.double().cpu()).abs().amax(-1, keepdim=True)
           + half_step(io, want))
+
+
+# ------------------------------------------------------------------ norm: values that are not finite stay where they are
+
+@pytest.mark.parametrize("order", [None, "odd"])
+@pytest.mark.parametrize("io,d,rot,layout", [("bf16", 64, 0, "half"), ("bf16", 64, 0, "pairs"), ("bf16", 64, 32, "half"), ("bf16", 64, 32, "pairs"),
+                                             ("bf16", 64, 6, "pairs"), ("bf16", 64, 6, "half"), ("f32", 128, 64, "half"), ("f32", 128, 64, "pairs"),
+                                             ("f32", 128, 2, "pairs"), ("bf16", 200, 100, "half"), ("f32", 256, 8, "half"), ("f32", 60, 28, "half")])
+def test_channels_that_do_not_turn_are_on_their_own(F, io, d, rot, layout, order):
+    """Without a norm, a channel that does not turn is x w forwards and g w backwards: an infinity or a NaN in one reaches
+    no other, and the gradient does not depend on x. The others keep the bits of a call without it."""
+    r = Draw(55)
+    (_, q), (_, g), (_, w) = r(2, 3, 20, d, dtype=IO[io], order=order), r(2, 3, 20, d, order=order), r(d)
+    freq = torch.rand(rot // 2, generator=r.g).cuda() if rot else None
+    kw = dict(wq=w, norm="none", rot=rot, layout=layout, freq=freq)
+    fwd = lambda: F.falcon_qknorm_fwd(q, None, **kw)[0].clone()
+    bwd = lambda: F.falcon_qknorm_bwd(q, None, g, None, **kw)
+    y, b = fwd(), bwd()
+    at = [(0, 0, 3, rot), (1, 2, 19, d - 1), (0, 1, 7, rot + (d - rot) // 2), (1, 0, 0, rot + 1)]
+    odd = [float("inf"), float("-inf"), float("nan"), float("inf")]
+    keep = [(q[i].clone(), g[i].clone()) for i in at]
+    for i, x in zip(at, odd):
+        q[i] = x
+    got = fwd()
+    for i, x in zip(at, odd):
+        assert got[i].isnan() if x != x else float(got[i]) == x * (1 if w[i[3]] > 0 else -1)
+        got[i] = y[i]
+    assert torch.equal(got, y)
+    back = bwd()
+    assert torch.equal(back["dq"], b["dq"])
+    channels = sorted({i[3] for i in at})
+    assert not back["dwq"][channels].isfinite().any()
+    rest = torch.ones(d, dtype=torch.bool)
+    rest[channels] = False
+    assert torch.equal(back["dwq"][rest], b["dwq"][rest])
+    for i, x, (qx, _) in zip(at, odd, keep):
+        q[i], g[i] = qx, x
+    back = bwd()
+    for i, x in zip(at, odd):
+        assert back["dq"][i].isnan() if x != x else float(back["dq"][i]) == x * (1 if w[i[3]] > 0 else -1)
+        back["dq"][i] = b["dq"][i]
+    assert torch.equal(back["dq"], b["dq"])
+
+
+@pytest.mark.parametrize("order", [None, "odd"])
+def test_norm_of_an_infinity(F, order):
+    """A row with an infinity has an infinite root: that channel is inf / inf, the others that do not turn with it are 0."""
+    r = Draw(56)
+    _, q = r(1, 2, 5, 64, order=order)
+    q[0, 1, 2, 40] = float("inf")
+    for rot, layout in ((0, "half"), (32, "half"), (32, "pairs"), (6, "pairs")):
+        y, _ = F.falcon_qknorm_fwd(q, None, rot=rot, layout=layout, freq=torch.ones(rot // 2, device="cuda") if rot else None)
+        row = y[0, 1, 2].clone()
+        assert row[40].isnan()
+        row[40] = 0
+        assert (row == 0).all()
+        y[0, 1, 2] = 0
+        assert y.isfinite().all()
