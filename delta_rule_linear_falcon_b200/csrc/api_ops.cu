@@ -187,15 +187,16 @@ falcon_status_t check_qknorm(const falcon_qknorm_args_t *a) {
     return FALCON_OK;
 }
 
-bool same_place(const falcon_view_t &x, const falcon_view_t &y) {
-    return x.p != y.p || (x.sb == y.sb && x.sh == y.sh && x.st == y.st);
+// In place: the same memory in the same order (the stride of an axis of one does not count).
+bool same_place(const falcon_view_t &x, const falcon_view_t &y, int B, int H, int T) {
+    return x.p != y.p || ((B <= 1 || x.sb == y.sb) && (H <= 1 || x.sh == y.sh) && (T <= 1 || x.st == y.st));
 }
 
 falcon_status_t check_qknorm_out(const falcon_qknorm_args_t *a) {
     const size_t es = elem_size(a->io_dtype);
     FALCON_TRY(check_view(a->q_out, a->B, a->Hq, a->T, a->d, es, true));
     FALCON_TRY(check_view(a->k_out, a->B, a->Hk, a->T, a->d, es, true));
-    FALCON_NEED(same_place(a->q, a->q_out) && same_place(a->k, a->k_out));
+    FALCON_NEED(same_place(a->q, a->q_out, a->B, a->Hq, a->T) && same_place(a->k, a->k_out, a->B, a->Hk, a->T));
     const long long tokens = (long long)a->B * a->T;
     const void *const q = start(a->q, tokens * a->Hq), *const k = start(a->k, tokens * a->Hk);
     const void *const q_out = start(a->q_out, tokens * a->Hq), *const k_out = start(a->k_out, tokens * a->Hk);
@@ -343,7 +344,7 @@ falcon_status_t falcon_qknorm_bwd(const falcon_qknorm_args_t *a, const falcon_qk
     FALCON_TRY(check_view(g->dk_out, a->B, a->Hk, a->T, a->d, 4, false));
     FALCON_TRY(check_view(g->dq, a->B, a->Hq, a->T, a->d, 4, true));
     FALCON_TRY(check_view(g->dk, a->B, a->Hk, a->T, a->d, 4, true));
-    FALCON_NEED(same_place(g->dq, g->dq_out) && same_place(g->dk, g->dk_out));
+    FALCON_NEED(same_place(g->dq, g->dq_out, a->B, a->Hq, a->T) && same_place(g->dk, g->dk_out, a->B, a->Hk, a->T));
     const long long tokens = (long long)a->B * a->T;
     const void *const q = start(a->q, tokens * a->Hq), *const k = start(a->k, tokens * a->Hk);
     const void *const q_up = start(g->dq_out, tokens * a->Hq), *const k_up = start(g->dk_out, tokens * a->Hk);

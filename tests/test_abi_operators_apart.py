@@ -5,6 +5,7 @@ import ctypes
 import pytest
 import torch
 
+from delta_rule_linear_falcon_b200 import falcon as F
 from test_abi_operators import (CUDA, INVALID, L, OK, UNSUPPORTED, conv, conv_grads, qknorm, qknorm_grads, scan, scan_grads,  # noqa: F401
                                 view)
 
@@ -123,3 +124,18 @@ def test_scan_backward_refuses_before_its_first_launch(L, kw):
             setattr(s, n, view((0x100000 if s is g else 0x200000) + 0x1000 * i, kw["B"], kw["H"], kw["T"], d))
     assert L.falcon_scan_bwd_workspace_size(R(a)) > 1 << 40
     assert L.falcon_scan_bwd(R(a), R(g), 0x10000, (1 << 64) - 16, None) == UNSUPPORTED
+
+
+@HERE
+def test_in_place_whatever_the_stride_of_an_axis_of_one(L):
+    """A single token's rows seen as (B, T, H, d) transposed and as (B, H, T, d): the same memory in the same order."""
+    a = qknorm(T=1)
+    a.q, a.q_out = F.FalconView(0x1000, 192, 64, 192), F.FalconView(0x1000, 192, 64, 64)
+    a.k, a.k_out = F.FalconView(0x2000, 64, 64, 64), F.FalconView(0x2000, 64, 7, 0)
+    assert L.falcon_qknorm_fwd(R(a), None) == CUDA
+    g = F.FalconQknormGrads()
+    g.dq_out, g.dq, g.dk_out, g.dk = a.q, a.q_out, a.k, a.k_out
+    b = qknorm(T=1, q=F.FalconView(0x11000, 192, 64, 64), k=F.FalconView(0x12000, 64, 64, 64))
+    assert L.falcon_qknorm_bwd(R(b), R(g), None, 0, None) == CUDA
+    a.q_out = F.FalconView(0x1000, 192, 65, 64)      # another order
+    assert L.falcon_qknorm_fwd(R(a), None) == INVALID
