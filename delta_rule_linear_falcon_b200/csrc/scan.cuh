@@ -10,12 +10,12 @@ namespace falcon {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A in units of log2 e, a decay being 2^(dt x). An A of -inf, or one that overflows here, is the most negative finite
-// value: a step of 0, as behind a sequence's end, times -inf would be NaN, and so would the sums of steps of 0 between
-// segments. Decays over steps above 2^-120 are 0 all the same.
+// A in units of log2 e, a decay being 2^(dt x). An infinite A, or one that overflows here, is the largest finite value of
+// its sign: a step of 0, as behind a sequence's end, times infinity would be NaN, and so would the sums of steps of 0
+// between segments. Decays over steps above 2^-120 are 0 all the same.
 __device__ __forceinline__ float decay_rate(float a) {
     const float x = a * kLog2e;
-    return x < -FLT_MAX ? -FLT_MAX : x;   // NaN stays
+    return x < -FLT_MAX ? -FLT_MAX : x > FLT_MAX ? FLT_MAX : x;   // NaN stays
 }
 
 constexpr int kScanThreads = 128;

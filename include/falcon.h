@@ -400,8 +400,9 @@ FALCON_API falcon_status_t falcon_conv_bwd(const falcon_conv_args_t *args, const
  *   S_t[i,c]  = exp(dt_t[i] A[i,c]) S_{t-1}[i,c] + dt_t[i] v_t[i] k_t[c]
  *   o_t[i]    = (sum_c S_t[i,c] q_t[c] + D[i] v_t[i]) silu(z_t[i])
  * (the terms of D, delta_bias and z only where those are given). dt A <= 0 is a precondition: the
- * decays lie in [0, 1]; it is not checked per element. An A below -3.4e38 / log2(e), -inf among them, counts as
- * that value: its decay is 0 for every step above 2^-120, and 1 for a step of 0 (as for any other A).
+ * decays lie in [0, 1]; it is not checked per element. An A beyond 3.4e38 / log2(e) in size, infinities among them,
+ * counts as that value of its sign: its decay is 0 for every step above 2^-120, and 1 for a step of 0 (as for any
+ * other A).
  * The state, the decays and all sums are fp32.
  * Supported: 1 <= dk <= 128; any dv >= 1; token strides up to 2^28 elements; fp32 or bf16.
  * Workspace: with few channels the sequence is split into segments that run at once, in two

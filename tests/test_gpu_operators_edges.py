@@ -62,6 +62,29 @@ def test_scan_step_forgets(F):
     assert torch.equal(S, kept)
 
 
+@pytest.mark.parametrize("B,H,T,dk,dv,lengths", [(2, 2, 21, 16, 64, [21, 13]), (2, 1, 900, 5, 9, [900, 101])])
+def test_scan_forgets_with_steps_below_0(F, B, H, T, dk, dv, lengths):
+    """dt A <= 0 with both signs turned: A up to +inf, steps as they are given, all below 0."""
+    h, g, r = scan_inputs(53, "f32", B, H, T, dk, dv, False, True, True, True, None)
+    for x in (h, g):
+        x["delta"], x["A"] = -x["delta"], -x["A"]
+    for c, x in ((0, float("inf")), (2, 3e38)):
+        h["A"][:, :, c], g["A"][:, :, c] = 1e30, x
+    h["delta"], g["delta"] = h["delta"] - 2.0 ** -7, g["delta"] - 2.0 ** -7      # no step of 0
+    h["delta"] = g["delta"].double().cpu()
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    want, S_w = O.scan(**h, softplus=False, lengths=lengths)
+    bo, bS = scan_bound({**h, "delta": -h["delta"], "A": -h["A"]}, False, lengths, T)
+    o, S = F.falcon_scan_fwd(**g, softplus=False, lengths=n, o=torch.zeros(B, H, T, dv, device="cuda"))
+    close(o, want, bo, "o")
+    close(S, S_w, bS, "S")
+    dO, dO_g = r(B, H, T, dv)
+    got = F.falcon_scan_bwd(**g, dO=dO_g, softplus=False, lengths=n)
+    leaves = {k: v.clone().requires_grad_() for k, v in h.items() if v is not None}
+    outs = O.scan(**{k: leaves.get(k) for k in h}, softplus=False, lengths=lengths)
+    gradients_close(got, {"d" + k: v for k, v in O.gradients(outs, (dO, None), leaves).items()}, T)
+
+
 def test_scan_nan_in_A_is_seen(F):
     _, g, _ = scan_inputs(52, "f32", 1, 1, 12, 16, 8, True, False, False, True, None)
     g["A"][0, 3, 5] = float("nan")
