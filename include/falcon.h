@@ -327,6 +327,7 @@ FALCON_API falcon_status_t falcon_decode_step(int rule, int io_dtype, int N, int
  *    token of the sequence.
  *  - Sizes: T <= 2^30; B H and H d below 2^31 (also H dk and H dv); B H T d <= 2^50. Calls that would take more than
  *    2^31 - 1 blocks are UNSUPPORTED, and write nothing.
+ *  - fp32 arithmetic takes subnormal values for 0, exponentials and reciprocals are good to 2^-21.
  *  - Sums over tokens are taken in a fixed order: repeated calls give the same bits.
  *  - A workspace is used only while the call's kernels run on `stream`; calls that can overlap on the GPU (other
  *    streams, graphs replayed side by side) need workspaces of their own. The first call of the library on a device
@@ -366,7 +367,7 @@ FALCON_API falcon_status_t falcon_conv_fwd(const falcon_conv_args_t *args, falco
 
 /*
  * falcon_conv_step -- one token for B sequences: falcon_conv_fwd with T = 1, as one small kernel.
- * `state` and `state_out` are both required (the same memory updates the cache in place);
+ * `state` and `state_out` are both required for K > 1 (the same memory updates the cache in place);
  * `lengths` must be NULL. Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 FALCON_API falcon_status_t falcon_conv_step(const falcon_conv_args_t *args, falcon_stream_t stream);
@@ -480,7 +481,8 @@ FALCON_API falcon_status_t falcon_scan_bwd(const falcon_scan_args_t *args, const
  * then the first `rot` channels of n turn in pairs by the angle positions[b,t] freq[j]:
  *   pair j is (j, j + rot/2) for FALCON_ROT_HALF, (2j, 2j+1) for FALCON_ROT_PAIRS;
  *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin).
- * Angles are reduced in fp64, so far positions keep their accuracy; everything else is fp32.
+ * Angles are reduced in fp64, so far positions keep their accuracy; everything else is fp32: a row whose sum of
+ * squares is below 2^-126 (entries near 1e-19) counts as one of 0, above 2^128 (near 1e19) as infinite.
  * positions NULL: t. rot = 0: no rotation. Hk (or Hq) = 0 leaves out that tensor. q_out may be the
  * same memory as q with the same strides (likewise k). One token per sequence is T = 1.
  * Supported: 1 <= d <= 256; Hq, Hk <= 65536; rot even, 0 <= rot <= d; fp32 or bf16.
@@ -510,7 +512,8 @@ FALCON_API falcon_status_t falcon_qknorm_fwd(const falcon_qknorm_args_t *args, f
  * angles and xr = x / root:  dw = sum g xr;  u = g w;  dx = (u - xr mean(u xr)) / root (the sum in place
  * of the mean for FALCON_NORM_L2; dx = u for FALCON_NORM_NONE). args->q_out and k_out are ignored.
  * dq may be the same memory as dq_out with the same strides (likewise dk).
- * Workspace: falcon_qknorm_bwd_workspace_size(args) bytes, 16-byte aligned (0 without dwq and dwk).
+ * Workspace: falcon_qknorm_bwd_workspace_size(args) bytes, 16-byte aligned; none is needed when dwq and dwk are
+ * both NULL (which the size, that of the forward arguments, does not know).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
  */
 typedef struct {

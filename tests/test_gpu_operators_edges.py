@@ -193,3 +193,19 @@ def test_norm_of_an_infinity(F, order):
         assert (row == 0).all()
         y[0, 1, 2] = 0
         assert y.isfinite().all()
+
+
+@pytest.mark.parametrize("d,order", [(64, None), (64, "odd"), (3, None)])
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_range_of_the_sum_of_squares(F, d, order, norm):
+    """eps = 0: entries whose squares fp32 holds are normalised, below that a row counts as 0, above as infinite."""
+    r = Draw(57)
+    x, q = r(1, 4, 1, d, order=order, make=lambda t: t.sign() + t / 8)
+    scale = torch.tensor([2.0 ** -62, 2.0 ** 59, 2.0 ** -70, 2.0 ** 66]).view(1, 4, 1, 1)
+    q *= scale.cuda()
+    y, _ = F.falcon_qknorm_fwd(q, None, norm=norm, eps=0.0)
+    want = O.qknorm(x * scale.double(), norm=norm, eps=0.0)
+    close(y[:, :2], want[:, :2], 2.0 ** -18 * want[:, :2].abs().amax(-1, keepdim=True))
+    assert (y[:, 2:] == 0).all()
+    g = F.falcon_qknorm_bwd(q, None, torch.ones(1, 4, 1, d, device="cuda"), None, norm=norm, eps=0.0)["dq"]
+    assert g.isfinite().all() and (g[:, 2:] == 0).all()
