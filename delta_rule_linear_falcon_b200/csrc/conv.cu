@@ -7,15 +7,19 @@
 // so every access of a warp is whole lines, whichever of token-major and head-major the two views are.
 // The inputs come ahead of their use through a ring in shared memory (kStages batches of kConvBatch tokens,
 // asynchronous copies into places that only the copying thread reads, so no barrier): bytes in flight cost no
-// registers. Eight bytes a thread rather than 16 leave registers for four blocks an SM (B8 H16 T4096 d128 bf16: 59 us
-// against 72). One channel a thread (V = 1): a batch's loads are in flight together (the same case off alignment: 124 us
-// against 59). A run re-reads its K - 1 first inputs (from L2). 53 us of kernel there, 5.1 TB/s: the exponential unit
-// (two of its operations for each silu) is at 63% and the instruction slots at 65%.
+// registers. Eight bytes a thread rather than 16 leave registers for four blocks an SM (B8 H16 T4096 d128 bf16: 57 us
+// against 72 before the runs were fitted to the SMs, 55 since). One channel a thread (V = 1): a batch's loads are in
+// flight together (the same case off alignment: 123 us). A run re-reads its K - 1 first inputs (from L2). 53 us of kernel
+// there, 5.1 TB/s: the exponential unit (two of its operations for each silu) is at 64% and the instruction slots at
+// 65%. K = 8, whose window and weights leave two blocks an SM: 75 us.
 // Backward: the same walk with a second window, of dp: step t needs x_{t-K+1..t} for p_t and act', adds
 // dp_t x to dw, and emits dx_{t-K+1} = sum_j w_j dp_{t-j}. The walk goes K - 1 tokens past the run
 // (dp there is formed again by the next run). dw and dbias: registers, then the block's shared memory,
 // then one row of partial sums for each block, summed in a fixed order by a second launch. B4 H16 T4096 d128 bf16:
-// 71 us and 5 us of kernels for 336 MB (51 us at the copy rate), 139 us in all off alignment.
+// 73 us and 6 us of kernels for 336 MB (51 us at the copy rate), 140 us in all off alignment. Eighty registers and 21
+// warps an SM, instruction slots at 57%: bound by latency. K = 5 82 us in all, K = 8 111 us, two blocks an SM. Short
+// sequences have a row of partial sums each, and blocks that T does not fill: B512 H16 T16 79 us against 25 at the
+// copy rate.
 #include "ops.cuh"
 
 namespace falcon {

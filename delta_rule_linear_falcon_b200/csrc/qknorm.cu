@@ -12,9 +12,10 @@
 // taken off in fp64), kept in registers over the walk, and the row addresses advance by one addition.
 // Where pointers, strides, d or rot are not multiples of a pack, V = 1: lane l owns channels l, l + 32, ..
 // and partners come through shared memory (the same case with rows off alignment: 182 us in all against 97).
+// Few heads a token pay badly for its angles: B4 H4+1 T8192 d128 32 us against 13 at the copy rate, B1 H8+2 18 against 6.
 // Backward: the same walk with the row turned back; dwq and dwk are summed per lane over the tokens of a
-// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 46 us and 6 us of kernels for
-// 210 MB (32 us at the copy rate), 81 us in all off alignment; bound by instruction latency, 16 warps an SM (the registers of two rows and their prefetch).
+// block, then over blocks by a second launch. B4 H16+4 T2048 d128: 44 us and 6 us of kernels for
+// 210 MB (32 us at the copy rate), 82 us in all off alignment; bound by instruction latency, 16 warps an SM (the registers of two rows and their prefetch).
 #include "ops.cuh"
 
 namespace falcon {

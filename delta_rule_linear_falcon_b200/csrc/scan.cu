@@ -19,10 +19,12 @@
 // cut into segments (scan_plan). A first launch runs every segment from a zero state and leaves its end
 // state E and the sum of its steps sd, from which the decay over the segment is exp(A sd); in the second
 // each segment joins the states before it, S <- exp(A sd_j) S + E_j, and runs with outputs.
-// Measured, bf16, dk = 16: B4 H16 T2048 dv128 (64 blocks unsplit) 183 us in 9 segments (unsplit, with the exponentials
-// of an earlier step-size formula, 398 us where 9 segments took 204); the exponential unit is at about 80% in the first
-// launch and 70% in the second. B1 T16384 dv2048: 352 us in 37 segments. 512 blocks unsplit (B32 H16 T1024 dv128,
-// the earlier formula): 458 us, 115 us for each 2^28 entries, whose exponentials alone are 58 us.
+// Measured, bf16, dk = 16: B4 H16 T2048 dv128 (64 blocks unsplit) 183 us in 9 segments, 383 us unsplit. B1 T16384
+// dv2048: 352 us in 37 segments. 512 blocks unsplit (B32 H16 T1024 dv128): 439 us, 110 us for each 2^28 entries, whose
+// exponentials alone are 58 us. No unit is full: in the launches of the split passes the exponential unit is at 66 to 69%
+// (a quarter of its work moved to the multiply-add pipes) and 71%, the instruction slots at 61 to 63% and 48%, the
+// multiply-add pipes at 60 to 63% and 40%, with 11 to 13 warps an SM (124 and 128 registers): too few of them to cover
+// each other's latencies. Two passes and four exponentials for three are the other half of the distance.
 #include "scan.cuh"
 
 namespace falcon {

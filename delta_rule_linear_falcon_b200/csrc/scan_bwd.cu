@@ -17,9 +17,11 @@
 // Step 3 sums over channels (dq, dk) and over columns (dv, ddelta, dz) of the same products. A thread owns
 // 4 channels x 4 columns, SL = dk / 4 lanes side by side: the first additions of either sum are fused
 // multiply-adds in registers, the rest 3 to 6 shuffles (lanes_sum) for 16 entries.
-// B2 H16 T2048 dv128 dk16, bf16, 332 us: 75 us for step 1, 12 for the joins, 258 for step 3 (alone), 4 for the sums. Step 3 is bound by
-// latency at 12 warps an SM (168 registers, half of them states; 70 KB of shared memory): its instruction slots are at
-// half, the exponential unit at 40%. Taken out one at a time, the channels' gradients at a segment's end were 55 us of it
+// B2 H16 T2048 dv128 dk16, bf16, 332 us. One launch at a time, each from cold caches: 77 us for step 1, 12 for the joins,
+// 261 for step 3, 6 for the sums (356 in all). Step 3 is bound by latency at 11 warps an SM (168 registers, half of them
+// states, 100 bytes spilled; 70 KB of shared memory): its instruction slots are at half, the exponential unit at 39%.
+// dk 4, 8 and 64 of the same tensors: 463, 309 and 1826 us (blocks of one and two warps, and 128 channels' products over
+// 64 columns). Taken out one at a time, the channels' gradients at a segment's end were 55 us of it
 // (45 since they are formed two tokens an instruction), the shuffled sums 28, the exponentials 19.
 #include "scan.cuh"
 
@@ -575,7 +577,9 @@ struct BwdSizes {
     long long floats;   // the workspace
 };
 
-// Turns that `blocks` blocks take at three an SM (what the registers of steps 1 and 3 allow).
+// Turns that `blocks` blocks take at three an SM: what registers and shared memory allow steps 1 and 3 for dk from 9 to
+// 32. (Shared memory leaves five blocks an SM for dk <= 4, four for dk <= 8, two for dk <= 64 and one above; they are
+// planned the same way.)
 long long turns(long long blocks) { return (blocks + 148 * 3 - 1) / (148 * 3); }
 
 // Segments of a walk: those with the shortest estimate in tokens' work of a block of step 3: its turns times a walk and
