@@ -187,9 +187,10 @@ falcon_status_t check_qknorm(const falcon_qknorm_args_t *a) {
     return FALCON_OK;
 }
 
-// In place: the same memory in the same order (the stride of an axis of one does not count).
+// In place: the same memory in the same order (the stride of an axis of one does not count), or nothing at all.
 bool same_place(const falcon_view_t &x, const falcon_view_t &y, int B, int H, int T) {
-    return x.p != y.p || ((B <= 1 || x.sb == y.sb) && (H <= 1 || x.sh == y.sh) && (T <= 1 || x.st == y.st));
+    if ((long long)B * H * T == 0) return true;
+    return x.p != y.p || ((B == 1 || x.sb == y.sb) && (H == 1 || x.sh == y.sh) && (T == 1 || x.st == y.st));
 }
 
 falcon_status_t check_qknorm_out(const falcon_qknorm_args_t *a) {

@@ -139,3 +139,14 @@ def test_in_place_whatever_the_stride_of_an_axis_of_one(L):
     assert L.falcon_qknorm_bwd(R(b), R(g), None, 0, None) == CUDA
     a.q_out = F.FalconView(0x1000, 192, 65, 64)      # another order
     assert L.falcon_qknorm_fwd(R(a), None) == INVALID
+
+
+@HERE
+@pytest.mark.parametrize("kw", [dict(B=0), dict(T=0)])
+def test_nothing_is_in_place(L, kw):
+    """Empty tensors of torch all have the address 0, whatever their strides."""
+    none = F.FalconView(0, 640, 64, 192)
+    a = qknorm(**kw, q=none, k=none, q_out=F.FalconView(0, 640, 10, 64), k_out=F.FalconView(0, 640, 640, 64))
+    assert L.falcon_qknorm_fwd(R(a), None) == OK
+    g = qknorm_grads(dq_out=none, dk_out=none, dq=F.FalconView(0, 640, 10, 64), dk=F.FalconView(0, 640, 640, 64), dwq=0x9000)
+    assert L.falcon_qknorm_bwd(R(a), R(g), None, 0, None) == CUDA

@@ -209,3 +209,58 @@ def test_range_of_the_sum_of_squares(F, d, order, norm):
     assert (y[:, 2:] == 0).all()
     g = F.falcon_qknorm_bwd(q, None, torch.ones(1, 4, 1, d, device="cuda"), None, norm=norm, eps=0.0)["dq"]
     assert g.isfinite().all() and (g[:, 2:] == 0).all()
+
+
+# ------------------------------------------------------------------ inputs that repeat, and problems of nothing
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_inputs_repeated_along_an_axis(F, io, axis):
+    """A stride of 0 along batch, heads or tokens: the bits of a call on copies, forwards and backwards."""
+    r = Draw(58)
+    size = [3, 4, 37]
+    one = [1 if i == axis else n for i, n in enumerate(size)]
+
+    def pair(d, dt=IO[io]):
+        x = r(*one, d, dtype=dt)[1].expand(*size, d)
+        return x, x.contiguous()
+
+    def same(call, *args):
+        a, b = (call(*(t[i] for t in args)) for i in (0, 1))
+        for x, y in zip(*((t.values() if isinstance(t, dict) else t for t in (a, b)))):
+            assert (x is None) == (y is None) and (x is None or torch.equal(x, y))
+
+    x, dy = pair(32), pair(32, torch.float32)
+    w = r(4, 32, 4)[1]
+    same(lambda x: F.falcon_conv_fwd(x, w, want_state=True), x)
+    same(lambda x, dy: F.falcon_conv_bwd(x, w, dy), x, dy)
+    freq = torch.rand(16, generator=r.g).cuda()
+    same(lambda x: F.falcon_qknorm_fwd(x, None, rot=32, freq=freq), x)
+    same(lambda x, dy: F.falcon_qknorm_bwd(x, None, dy, None, wq=w[0, :, 0].contiguous(), rot=32, freq=freq), x, dy)
+    A, D = -torch.rand(4, 32, 16, generator=r.g).cuda(), r(4, 32)[1]
+    q, k, delta, z = pair(16), pair(16), pair(32), pair(32)
+    same(lambda q, k, v, e, z: F.falcon_scan_fwd(q, k, v, e, A, D=D, z=z), q, k, x, delta, z)
+    same(lambda q, k, v, e, z, g: F.falcon_scan_bwd(q, k, v, e, A, g, D=D, z=z), q, k, x, delta, z, dy)
+
+
+@pytest.mark.parametrize("B,H,T", [(0, 2, 5), (2, 3, 0), (0, 1, 0)])
+def test_nothing_to_do(F, B, H, T):
+    """No sequences, heads or tokens: outputs of that shape, and parameters' gradients of 0."""
+    z = lambda *s: torch.zeros(*s, device="cuda")
+    x, w = z(B, H, T, 8), z(H, 8, 4)
+    y, tail = F.falcon_conv_fwd(x, w, want_state=True)
+    assert y.shape == x.shape and tail.shape == (B, H, 3, 8)
+    assert F.falcon_conv_step(z(B, H, 8), w, tail).shape == (B, H, 8)
+    g = F.falcon_conv_bwd(x, w, x, bias=z(H, 8), state=tail)
+    assert g["dw"].shape == w.shape and not g["dw"].any() and not g["dbias"].any()
+    A = z(H, 8, 4)
+    q = z(B, H, T, 4)
+    o, S = F.falcon_scan_fwd(q, q, x, x, A)
+    assert o.shape == x.shape and S.shape == (B, H, 8, 4)
+    assert F.falcon_scan_step(z(B, H, 4), z(B, H, 4), z(B, H, 8), z(B, H, 8), A, S).shape == (B, H, 8)
+    g = F.falcon_scan_bwd(q, q, x, x, A, x, D=z(H, 8), delta_bias=z(H, 8), S0=S)
+    assert not g["dA"].any() and not g["dD"].any() and not g["ddelta_bias"].any()
+    a, b = F.falcon_qknorm_fwd(x, x, rot=8, freq=z(4))
+    assert a.shape == b.shape == x.shape
+    g = F.falcon_qknorm_bwd(x, x, x, x, wq=z(8), wk=z(8), rot=8, freq=z(4))
+    assert not g["dwq"].any() and not g["dwk"].any()
