@@ -53,7 +53,7 @@ ConvShape conv_shape(const falcon_conv_args_t &a, int V, long long slots) {
     s.ncb = (packs + s.bx - 1) / s.bx;
     long long run = kLongest;
     for (int turns = 1; turns <= 8; ++turns) {
-        const long long rows = s.ncb * (a.B > 0 ? a.B : 1), tiles = slots * turns > rows ? slots * turns / rows : 1;
+        const long long all = s.ncb * a.B, rows = all > 0 ? all : 1, tiles = slots * turns > rows ? slots * turns / rows : 1;
         run = (a.T + tiles * s.by - 1) / (tiles * s.by);
         if (run <= kLongest) break;
     }

@@ -1,6 +1,8 @@
 """Host checks of the operators around the memory: an output that starts where an input or another output does is
 refused (no kernel runs), except where the header allows it."""
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -150,3 +152,31 @@ def test_nothing_is_in_place(L, kw):
     assert L.falcon_qknorm_fwd(R(a), None) == OK
     g = qknorm_grads(dq_out=none, dk_out=none, dq=F.FalconView(0, 640, 10, 64), dk=F.FalconView(0, 640, 640, 64), dwq=0x9000)
     assert L.falcon_qknorm_bwd(R(a), R(g), None, 0, None) == CUDA
+
+
+def test_sizes_of_nothing(L):
+    """Workspace sizes of no sequences, heads or tokens (in a process of its own: without heads the convolution's once
+    divided by zero)."""
+    code = """
+import sys; sys.path[:0] = {path!r}
+import ctypes
+from test_abi_operators import B, F, conv, qknorm, scan
+L = F.lib()
+R = ctypes.byref
+for b in (0, 2):
+    for h in (0, 3):
+        for t in (0, 1, 10):
+            n = F.FalconView()
+            if b * h == 0:
+                assert L.falcon_conv_bwd_workspace_size(R(conv(B=b, H=h, T=t, x=n, w=None))) == 0, (b, h, t)
+                assert L.falcon_scan_bwd_workspace_size(R(scan(B=b, H=h, T=t, q=n, k=n, v=n, delta=n, A=None))) == 0, (b, h, t)
+                assert L.falcon_qknorm_bwd_workspace_size(R(qknorm(B=b, Hq=h, Hk=0, T=t, q=n, k=n, freq=None))) == 0, (b, h, t)
+                assert L.falcon_scan_workspace_size(R(scan(B=b, H=h, T=t, q=n, k=n, v=n, delta=n, A=None))) == 0, (b, h, t)
+            else:
+                L.falcon_conv_bwd_workspace_size(R(conv(B=b, H=h, T=t)))
+                L.falcon_scan_bwd_workspace_size(R(scan(B=b, H=h, T=t)))
+                L.falcon_qknorm_bwd_workspace_size(R(qknorm(B=b, Hq=h, T=t)))
+print("all")
+"""
+    r = subprocess.run([sys.executable, "-c", code.format(path=sys.path)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout == "all\n", (r.returncode, r.stderr[-500:])

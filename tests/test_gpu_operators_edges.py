@@ -243,7 +243,7 @@ def test_inputs_repeated_along_an_axis(F, io, axis):
     same(lambda q, k, v, e, z, g: F.falcon_scan_bwd(q, k, v, e, A, g, D=D, z=z), q, k, x, delta, z, dy)
 
 
-@pytest.mark.parametrize("B,H,T", [(0, 2, 5), (2, 3, 0), (0, 1, 0)])
+@pytest.mark.parametrize("B,H,T", [(0, 2, 5), (2, 3, 0), (0, 1, 0), (2, 0, 5), (0, 0, 5), (1, 0, 0)])
 def test_nothing_to_do(F, B, H, T):
     """No sequences, heads or tokens: outputs of that shape, and parameters' gradients of 0."""
     z = lambda *s: torch.zeros(*s, device="cuda")
