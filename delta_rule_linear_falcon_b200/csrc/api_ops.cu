@@ -132,6 +132,8 @@ falcon_status_t check_conv_out(const falcon_conv_args_t *a) {
 
 // ---- scan
 
+constexpr int kMaxChannels = 0x7fffffff - 511;   // channel numbers of a block that dv does not fill stay in 31 bits
+
 // The scan's kernels take token strides of up to 2^28 elements (32 bits of bytes).
 bool far_tokens(const falcon_view_t &v, int T) { return v.p && T > 1 && v.st > (1LL << 28); }
 
@@ -139,7 +141,7 @@ falcon_status_t check_scan(const falcon_scan_args_t *a) {
     FALCON_NEED(a);
     FALCON_NEED(a->dk > 0);
     FALCON_TRY(check_sizes(a->io_dtype, a->B, a->H, a->T, a->dv));
-    if (a->dk > 128) return FALCON_ERR_UNSUPPORTED;
+    if (a->dk > 128 || a->dv > kMaxChannels) return FALCON_ERR_UNSUPPORTED;
     FALCON_TRY(check_sizes(a->io_dtype, a->B, a->H, a->T, a->dk));
     if ((long long)a->B * a->H * a->dv > kMaxSpan / a->dk) return FALCON_ERR_UNSUPPORTED;
     FALCON_NEED((a->flags & ~FALCON_SCAN_SOFTPLUS) == 0);

@@ -45,7 +45,7 @@ struct ConvShape {
 ConvShape conv_shape(const falcon_conv_args_t &a, int V, long long slots) {
     constexpr long long kLongest = 160, kShortest = 8;
     ConvShape s;
-    s.nv = (a.d + V - 1) / V;
+    s.nv = (a.d - 1) / V + 1;
     const long long packs = (long long)a.H * s.nv;
     s.bx = 32;
     while (s.bx < kConvThreads && s.bx < packs) s.bx *= 2;
@@ -529,7 +529,7 @@ cudaError_t conv_fwd_io(const falcon_conv_args_t &a, const ConvShape &s, cudaStr
 
 template <typename IO, int V>
 cudaError_t conv_step_io(const falcon_conv_args_t &a, int num_sms, cudaStream_t st) {
-    const int nv = (a.d + V - 1) / V;
+    const int nv = (a.d - 1) / V + 1;
     const long long packs = (long long)a.H * nv, threads = (long long)num_sms * step_blocks(a.K) * kStepThreads;
     // sequences of a thread: the number with the shortest estimate, in turns of the threads that the SMs hold at once
     // (a thread's start, with its weights, costs about one sequence). For fp32, whose weights weigh half as much, up to two:

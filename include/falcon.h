@@ -405,7 +405,7 @@ FALCON_API falcon_status_t falcon_conv_bwd(const falcon_conv_args_t *args, const
  * counts as that value of its sign: its decay is 0 for every step above 2^-120, and 1 for a step of 0 (as for any
  * other A).
  * The state, the decays and all sums are fp32.
- * Supported: 1 <= dk <= 128; any dv >= 1; token strides up to 2^28 elements; fp32 or bf16.
+ * Supported: 1 <= dk <= 128; 1 <= dv <= 2^31 - 512; token strides up to 2^28 elements; fp32 or bf16.
  * Workspace: with few channels the sequence is split into segments that run at once, in two
  * launches (each segment from a zero state; then each from the joined states before it).
  * falcon_scan_workspace_size(args) bytes, 16-byte aligned, are needed for that, 0 where it does not

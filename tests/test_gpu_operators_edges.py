@@ -264,3 +264,24 @@ def test_nothing_to_do(F, B, H, T):
     assert a.shape == b.shape == x.shape
     g = F.falcon_qknorm_bwd(x, x, x, x, wq=z(8), wk=z(8), rot=8, freq=z(4))
     assert not g["dwq"].any() and not g["dwk"].any()
+
+
+@pytest.mark.parametrize("dv", [2 ** 31 - 512, 2 ** 31 - 513])
+def test_the_widest_scan(F, dv):
+    """One token of one head with as many channels as there may be, one column each: channel numbers and offsets at the end
+    of 31 bits, in rows of whole 16-byte words and of single elements."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    one = torch.ones(1, 1, 1, 1, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones(1, 1, 1, dv, dtype=torch.bfloat16, device="cuda")
+    delta = torch.zeros_like(v)
+    v[..., -1], delta[..., -1] = 3, 2
+    A = torch.zeros(1, dv, 1, device="cuda")
+    few = F.falcon_scan_fwd(one, one, v[..., -8:].contiguous(), delta[..., -8:].contiguous(), A[:, -8:].contiguous())
+    o, S = F.falcon_scan_fwd(one, one, v, delta, A)
+    assert torch.equal(o[..., -8:], few[0]) and torch.equal(S[:, :, -8:], few[1])
+    assert (o[..., :-1] == o[0, 0, 0, 0]).all() and (S[:, :, :-1] == S[0, 0, 0, 0]).all()
+    y = F.falcon_scan_step(one[:, :, 0], one[:, :, 0], v[:, :, 0], delta[:, :, 0], A, S)    # S twice the step now
+    want = F.falcon_scan_step(one[:, :, 0], one[:, :, 0], v[:, :, 0, -8:].contiguous(), delta[:, :, 0, -8:].contiguous(), A[:, -8:].contiguous(), few[1])
+    assert torch.equal(y[..., -8:], want) and torch.equal(S[:, :, -8:], few[1])
+    assert (y[..., :-1] == y[0, 0, 0]).all() and (S[:, :, :-1] == S[0, 0, 0, 0]).all()
