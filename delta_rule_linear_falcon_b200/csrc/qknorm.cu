@@ -162,7 +162,7 @@ template <int V>
 __device__ __forceinline__ f32x2 turning(f32x2 x, int p, int i, int rot) {
     float lo, hi;
     unpack2(x, lo, hi);
-    const int first = p * V + 4 * i;   // as channels of FALCON_ROT_PAIRS
+    const int first = p * V + 4 * i;
     return pack2(first < rot ? lo : 0.f, first + 2 < rot ? hi : 0.f);
 }
 
@@ -229,17 +229,21 @@ template <int LANES, int NV, bool HALF, bool SOME> struct Turn<1, LANES, NV, HAL
     }
 };
 
-// Which channels turn: none, each one, or some. A pair that does not turn must not see its partner (a sine of 0 times
-// infinity is NaN), and choosing costs registers, so the first two are compiled on their own.
-enum TurnKind : int { kTurnNone, kTurnAll, kTurnSome };
+// Which channels turn: none, each one, those of whole packs (as in halves they always are), or some. A pair that does not
+// turn must not see its partner (a sine of 0 times infinity is NaN), and choosing costs registers, so each is compiled on
+// its own; of single channels only the first two and the last.
+enum TurnKind : int { kTurnNone, kTurnAll, kTurnPacks, kTurnSome };
 
-// Blocks an SM that the last kind is held to (0: as it comes), measured on bf16 B8 H16+16 T4096 d128 with 64 channels
-// turned, in pairs: four 95 us, as it comes (three) 103; with d 64 and 6 turned, packs of four: six 51, as it comes 58. In
-// halves, where a pack turns or does not: as it comes 94, four 102. One channel a pack, d 199 fp32: four 93, as it comes 101.
+// Blocks an SM that the last two are held to (0: as it comes), measured on bf16 B8 H16+16 T4096. Some of a pack's pairs:
+// d64 with 6 turned, in packs of four, six 51 us, as it comes 58; in packs of eight four 95, as it comes (three) 103. Whole
+// packs: as it comes 94, four 102; fp32 B8 H8+8 in pairs five 88, as it comes (four) 90; in halves it comes with five.
+// One channel a pack, d 199 fp32: four 93, as it comes 101.
 constexpr int fwd_blocks(int es, int V, int NV, bool half, int turn) {
-    if (turn != kTurnSome) return 0;
+    if (turn < kTurnPacks) return 0;
     if (V == 1) return NV == 8 ? 4 : 0;
-    return half || NV > 1 ? 0 : V == 8 ? 4 : es == 2 ? 6 : 5;
+    if (NV > 1) return 0;
+    if (turn == kTurnPacks) return es == 4 && !half ? 5 : 0;
+    return V == 8 ? 4 : es == 2 ? 6 : 5;
 }
 
 template <typename IO, int V, int LANES, int NV, bool HALF, int TURN>
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(kNormThreads, fwd_blocks(sizeof(IO), V, NV, HA
                                 if (TURN == kTurnAll || (lane + m * LANES) * V < a.rot) {
                                     z1 = mul2(x2[m][i], s2[m][i]);
                                     z2 = mul2(x1[m][i], s1[m][i]);
-                                    if (TURN == kTurnSome && !HALF) {   // the last pack's pairs may turn in part
+                                    if (TURN == kTurnSome) {   // the last pack's pairs may turn in part
                                         z1 = turning<V>(z1, lane + m * LANES, i, a.rot);
                                         z2 = turning<V>(z2, lane + m * LANES, i, a.rot);
                                     }
@@ -493,12 +497,12 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 2 : 1) qknorm_bwd_kern
                             for (int i = 0; i < Q; ++i) {
                                 u1[m][i] = pack2(u[m][2 * i], u[m][2 * i + 1]);
                                 u2[m][i] = pack2(u[m][H + 2 * i], u[m][H + 2 * i + 1]);
-                                if (TURN == kTurnAll || (TURN == kTurnSome && (lane + m * LANES) * V < a.rot)) {
+                                if (TURN == kTurnAll || (TURN != kTurnNone && (lane + m * LANES) * V < a.rot)) {
                                     const f32x2 c = pack2(turn.c[m][2 * i], turn.c[m][2 * i + 1]);
                                     const f32x2 sn = pack2(turn.s[m][2 * i], turn.s[m][2 * i + 1]);
                                     const f32x2 ns = pack2(-turn.s[m][2 * i], -turn.s[m][2 * i + 1]);
                                     f32x2 z1 = mul2(u2[m][i], ns), z2 = mul2(u1[m][i], sn);
-                                    if (TURN == kTurnSome && !HALF) {   // the last pack's pairs may turn in part
+                                    if (TURN == kTurnSome) {   // the last pack's pairs may turn in part
                                         z1 = turning<V>(z1, lane + m * LANES, i, a.rot);
                                         z2 = turning<V>(z2, lane + m * LANES, i, a.rot);
                                     }
@@ -649,7 +653,10 @@ cudaError_t norm_run(const falcon_qknorm_args_t &a, const falcon_qknorm_grads_t 
     } else if (a.rot == a.d && !(g && a.norm == FALCON_NORM_NONE)) {   // (without a norm the gradient has to choose as well)
         return norm_launch<IO, V, LANES, NV, HALF, kTurnAll>(a, g, part, st);
     }
-    return norm_launch<IO, V, LANES, NV, HALF, kTurnSome>(a, g, part, st);
+    if constexpr (V > 1 && !HALF) {
+        if (a.rot % V == 0) return norm_launch<IO, V, LANES, NV, HALF, kTurnPacks>(a, g, part, st);
+    }
+    return norm_launch<IO, V, LANES, NV, HALF, (V > 1 && HALF) ? kTurnPacks : kTurnSome>(a, g, part, st);
 }
 
 template <typename IO, int V, bool HALF>
